@@ -63,7 +63,8 @@ typedef enum {
     SAGE_ERR_WORKSPACE = 4,     /* workspace missing or smaller than sage_workspace_size() */
     SAGE_ERR_CUDA = 5,          /* a CUDA runtime call failed (see sage_last_cuda_error) */
     SAGE_ERR_TIMEOUT = 6,       /* device: a bounded wait inside a kernel gave up */
-    SAGE_ERR_BAD_SEQLENS = 7    /* device: cu_seqlens not monotonic / out of range */
+    SAGE_ERR_BAD_SEQLENS = 7,   /* device: cu_seqlens not monotonic / out of range */
+    SAGE_ERR_BAD_PAGE = 8       /* device: a block table entry is not a page of the cache */
 } sage_status_t;
 
 enum { SAGE_PV_FP16 = 0, SAGE_PV_FP8 = 1 };
@@ -319,6 +320,136 @@ SAGE_API sage_status_t sage_attn_decode_quantized(const int8_t *q_i8, const floa
                                                   int Nq, int Nk, int d, int causal,
                                                   float sm_scale, int flags, void *workspace,
                                                   size_t ws_bytes, sage_stream_t stream);
+
+/*
+ * Rotary positions and the paged 4-bit cache. What a serving loop calls around the
+ * attention: sage_rope rotates queries and keys; sage_kv4_append rotates new queries and
+ * keys and writes keys and values into a paged cache in 4 bits; sage_attn_kv4 is the
+ * attention of a few new queries per sequence over that cache; sage_kv4_gather reads the
+ * cache back as 16-bit tensors, e.g. for sage_attn_varlen_fwd_kv of a prefill chunk.
+ * Tensors are fp16 (dtype SAGE_F16) or bf16 (SAGE_BF16), head dim 64 or 128.
+ *
+ * Rotation: pair i of the first rot_dim channels of a head at position p becomes
+ * y0 = x0 c - x1 s, y1 = x1 c + x0 s, c = cos(p freqs[i]) mscale, s = sin(p freqs[i])
+ * mscale; the pairs are (i, i + rot_dim/2), or (2i, 2i+1) with SAGE_ROPE_INTERLEAVED;
+ * channels from rot_dim on are unchanged. SAGE_ROPE_INVERSE takes -s: the transpose, which
+ * is the gradient of the rotation. Angles, sines and cosines are computed in 64 bits, the
+ * rotation in fp32, the result is rounded once. rot_dim is a multiple of 16, at most d.
+ *
+ * Strides are host arrays in elements, multiples of 8; the channels of a head are
+ * contiguous and its first one 16-byte aligned.
+ */
+enum { SAGE_F16 = 0, SAGE_BF16 = 1 };
+enum { SAGE_ROPE_INTERLEAVED = 1, SAGE_ROPE_INVERSE = 2 };
+enum {
+    SAGE_ROPE_PLAIN = 0,   /* f_i = base^(-2i/rot_dim) */
+    SAGE_ROPE_LINEAR = 1,  /* f_i / factor: positions interpolated */
+    SAGE_ROPE_BASE = 2,    /* base scaled by factor^(rot_dim/(rot_dim-2)): the slowest pair
+                              is divided by factor, the fastest kept */
+    SAGE_ROPE_PARTS = 3    /* pairs that turn more than beta_fast times over the
+                              original_len trained positions keep f_i, those that turn less
+                              than beta_slow times get f_i / factor, a linear ramp over i
+                              between; mscale = 0.1 ln(factor) + 1 */
+};
+
+/*
+ * The pairs' angles per position, freqs[rot_dim/2] IN HOST MEMORY, and (mscale may be NULL)
+ * the factor on cos and sin that belongs to them: 1, or SAGE_ROPE_PARTS's. factor >= 1,
+ * original_len > 0 and beta_fast > beta_slow > 0 are read where the scaling uses them. No
+ * CUDA call is made; the caller copies freqs to the device.
+ */
+SAGE_API sage_status_t sage_rope_freqs(double *freqs, double *mscale, int rot_dim, double base,
+                                       int scaling, double factor, double original_len,
+                                       double beta_fast, double beta_slow);
+
+/*
+ * q [B,Hq,N,d] -> q_out and k [B,Hk,N,d] -> k_out, rotated by positions (int32 on the
+ * device, [B,N] with pos_stride elements between batches, 0 for [N] shared by all; NULL:
+ * 0 .. N-1). strides: {batch, head, token} of q, q_out, k, k_out (12 values), or NULL for
+ * dense tensors. Packed [T,H,d] tensors are B = 1, N = T with strides {0, d, H*d}. k may be
+ * NULL (Hk = 0). q_out = q with the same strides rotates in place; other overlaps are not
+ * allowed. freqs: double [rot_dim/2] on the device. flags: SAGE_ROPE_INTERLEAVED |
+ * SAGE_ROPE_INVERSE. Allocates nothing.
+ */
+SAGE_API sage_status_t sage_rope(const void *q, void *q_out, const void *k, void *k_out,
+                                 const int32_t *positions, const double *freqs, int dtype, int B,
+                                 int N, int Hq, int Hk, int d, int rot_dim, int64_t pos_stride,
+                                 const int64_t *strides, double mscale, int flags,
+                                 sage_stream_t stream);
+
+/*
+ * The 4-bit cache. Each token of a key or value head is cut into groups of 64 channels. With
+ * lo and hi a group's least and greatest value: step = fp16((hi - lo) / 15), low = fp16(lo),
+ * code = round-half-even((x - low) / step) clamped to 0..15 (0 where step is 0), in fp32 (the
+ * division by 15 as a product with its fp32 reciprocal); the group stands for low + code * step. A group that holds a NaN, an infinity or a value past
+ * fp16's range stands for non-finite values, and so does an output that sees it.
+ *
+ * cache [num_pages, Hkv, sage_kv4_page_bytes(page_size, d)] bytes, 16-byte aligned. A page of
+ * a head holds page_size tokens (a power of two, 16 to 256): key codes [page_size][d/2]
+ * (channel 2i in the low half of byte i), value codes, then (step, low) of the keys' groups
+ * as fp16 [page_size][d/64][2], and of the values'. 4.5 bits per element in all.
+ *
+ * The sequences of a call: kv_lens int32 [nseq], the tokens sequence s holds, those of this
+ * call included; block_table int32 [nseq, max_pages], token j of s lies in row j % page_size
+ * of page block_table[s][j / page_size]; cu_seqlens int32 [nseq+1], the rows of the packed
+ * tensors (total rows) that are the last tokens of s, or NULL: total / nseq rows each (nseq
+ * must divide total). All on the device; none is read on the host, so a call can be captured
+ * in a graph and replayed with new contents. Rows past cu_seqlens[nseq] (padding) are not
+ * read and not written. Malformed lengths (SAGE_ERR_BAD_SEQLENS) or table entries outside
+ * [0, num_pages) (SAGE_ERR_BAD_PAGE) set the device status word; nothing outside the buffers
+ * is touched; the outputs (cache rows) of that sequence, or of all sequences where
+ * cu_seqlens is malformed, are then undefined.
+ */
+SAGE_API size_t sage_kv4_page_bytes(int page_size, int d);
+
+/*
+ * Append: rows of k and v [total,Hkv,d] become the last tokens of their sequences, k rotated
+ * by the tokens' positions (rot_dim = 0: not at all) and, with k_mean (fp32 [Hkv,d], e.g. the
+ * channel means of calibration prompts), lessened by it after the rotation: attention does
+ * not change when every key of a head is moved by the same vector, and a key's 4-bit range is
+ * not spent on a channel offset (the smoothing of step 1 for a cache that grows). q
+ * [total,Hq,d] is rotated to q_out alike, or NULL. strides: {token, head} of k, v, q, q_out
+ * (8 values), or NULL for contiguous tensors. q_out may be q with the same strides. The pages
+ * of a call's new tokens must belong to one sequence each. Allocates nothing.
+ */
+SAGE_API sage_status_t sage_kv4_append(void *cache, const int32_t *block_table,
+                                       const int32_t *kv_lens, const int32_t *cu_seqlens,
+                                       const void *k, const void *v, const void *q, void *q_out,
+                                       const double *freqs, const float *k_mean, int dtype,
+                                       int nseq, int total, int Hq, int Hkv, int d,
+                                       int page_size, int num_pages, int max_pages, int rot_dim,
+                                       const int64_t *strides, double mscale, int flags,
+                                       sage_stream_t stream);
+
+/*
+ * Gather: the last tokens of every sequence as k_out and v_out [total, Hkv*rep, d], each head
+ * written rep times side by side (for attention entry points that take as many key heads as
+ * query heads). With cu_seqlens the running sum of kv_lens: all of them. Allocates nothing.
+ */
+SAGE_API sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_table,
+                                       const int32_t *kv_lens, const int32_t *cu_seqlens,
+                                       void *k_out, void *v_out, int dtype, int nseq, int total,
+                                       int Hkv, int rep, int d, int page_size, int num_pages,
+                                       int max_pages, sage_stream_t stream);
+
+/*
+ * Attention of q [total,Hq,d] (strides q_strides {token, head}, NULL: contiguous) over the
+ * cache: query head h reads key head h / (Hq/Hkv). A sequence has at most max_q <=
+ * SAGE_DECODE_MAX_Q queries; its query i of n sees keys j <= kv_len - n + i (causal) or all
+ * of them. out [total,Hq,d]; lse (fp32 [total,Hq], natural log of the sum of exp, or NULL).
+ * A query that sees no key gets zeros and -inf. sm_scale <= 0 selects 1/sqrt(d). Scores and
+ * softmax are fp32; probabilities enter the value product as two fp16 terms (21 bits).
+ * Results do not depend on timing. workspace: device memory of
+ * sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) bytes, 16-byte aligned, whose contents
+ * need not be kept between calls; calls that can overlap need one each.
+ */
+SAGE_API size_t sage_attn_kv4_workspace_size(int Hq, int Hkv, int max_q, int d);
+SAGE_API sage_status_t sage_attn_kv4(const void *q, const void *cache, const int32_t *block_table,
+                                     const int32_t *kv_lens, const int32_t *cu_seqlens, void *out,
+                                     float *lse, int dtype, int nseq, int total, int max_q, int Hq,
+                                     int Hkv, int d, int page_size, int num_pages, int max_pages,
+                                     int causal, float sm_scale, const int64_t *q_strides,
+                                     void *workspace, size_t ws_bytes, sage_stream_t stream);
 
 /*
  * Debug: the integer score tiles S = q_i8 k_i8^T (int32, [B,H,N,N]) exactly as the

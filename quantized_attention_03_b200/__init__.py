@@ -29,12 +29,21 @@ SAGE_ERR_WORKSPACE = 4
 SAGE_ERR_CUDA = 5
 SAGE_ERR_TIMEOUT = 6
 SAGE_ERR_BAD_SEQLENS = 7
+SAGE_ERR_BAD_PAGE = 8
 SAGE_PV_FP16 = 0
 SAGE_PV_FP8 = 1
 SAGE_SMOOTH_K = 1     # flags of the fused entry points' smooth_k argument
 SAGE_SMOOTH_V = 2
 SAGE_SMOOTH_Q = 4
 SAGE_QK_FINE = 8
+SAGE_F16 = 0          # dtype of the rotary and 4-bit cache entry points
+SAGE_BF16 = 1
+SAGE_ROPE_INTERLEAVED = 1   # flags of the rotations
+SAGE_ROPE_INVERSE = 2
+SAGE_ROPE_PLAIN = 0         # scalings of sage_rope_freqs
+SAGE_ROPE_LINEAR = 1
+SAGE_ROPE_BASE = 2
+SAGE_ROPE_PARTS = 3
 
 Q_BLOCK = 128
 K_BLOCK = 64
@@ -44,6 +53,8 @@ DECODE_MAX_Q = 16   # SAGE_DECODE_MAX_Q: most queries sage_attn_decode_quantized
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
+_L = ctypes.c_int64
 _Z = ctypes.c_size_t
 _S = ctypes.c_int  # sage_status_t
 SIGNATURES = {
@@ -60,6 +71,15 @@ SIGNATURES = {
     "sage_attn_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "sage_attn_decode_quantized": (_S, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I,
                                         _P, _Z, _P]),
+    "sage_rope_freqs": (_S, [_P, _P, _I, _D, _I, _D, _D, _D, _D]),
+    "sage_rope": (_S, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _L, _P, _D, _I, _P]),
+    "sage_kv4_page_bytes": (_Z, [_I, _I]),
+    "sage_kv4_append": (_S, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                             _I, _I, _P, _D, _I, _P]),
+    "sage_kv4_gather": (_S, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "sage_attn_kv4_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "sage_attn_kv4": (_S, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                           _F, _P, _P, _Z, _P]),
     "sage_quant_qk": (_S, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "sage_quant_qk_ws": (_S, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P]),
     "sage_quant_qk_varlen": (_S, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P]),
@@ -189,6 +209,64 @@ def sage_attn_decode_quantized(q_i8, q_scale, k_i8, k_scale, v, out, B, H, Nq, N
     return _call("sage_attn_decode_quantized", _ptr(q_i8), _ptr(q_scale), _ptr(k_i8),
                  _ptr(k_scale), _ptr(v), _ptr(out), B, H, Nq, Nk, d, int(causal),
                  float(sm_scale), int(flags), _ptr(workspace), int(ws_bytes), _stream(stream))
+
+
+def _i64s(x):
+    """A host array of int64 (or None) as sage.h's strides arguments take it."""
+    return None if x is None else (ctypes.c_int64 * len(x))(*x)
+
+
+def sage_rope_freqs(freqs, mscale, rot_dim, base, scaling, factor, original_len, beta_fast,
+                    beta_slow):
+    """freqs, mscale: host addresses (int, ctypes array or CPU tensor; mscale may be None)."""
+    freqs = freqs if isinstance(freqs, ctypes.Array) else _ptr(freqs)
+    return _call("sage_rope_freqs", freqs,
+                 mscale if isinstance(mscale, ctypes.Array) else _ptr(mscale), rot_dim,
+                 float(base), int(scaling), float(factor), float(original_len), float(beta_fast),
+                 float(beta_slow))
+
+
+def sage_rope(q, q_out, k, k_out, positions, freqs, dtype, B, N, Hq, Hk, d, rot_dim, pos_stride,
+              strides, mscale, flags, stream=None):
+    """strides: 12 integers or None (see sage.h)."""
+    return _call("sage_rope", _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(positions),
+                 _ptr(freqs), dtype, B, N, Hq, Hk, d, rot_dim, pos_stride, _i64s(strides), mscale,
+                 flags, _stream(stream))
+
+
+def sage_kv4_page_bytes(page_size, d) -> int:
+    return int(lib().sage_kv4_page_bytes(page_size, d))
+
+
+def sage_kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q, q_out, freqs, k_mean, dtype,
+                    nseq, total, Hq, Hkv, d, page_size, num_pages, max_pages, rot_dim, strides,
+                    mscale, flags, stream=None):
+    """strides: 8 integers or None (see sage.h)."""
+    return _call("sage_kv4_append", _ptr(cache), _ptr(block_table), _ptr(kv_lens),
+                 _ptr(cu_seqlens), _ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(freqs),
+                 _ptr(k_mean), dtype, nseq, total, Hq, Hkv, d, page_size, num_pages, max_pages,
+                 rot_dim, _i64s(strides), mscale, flags, _stream(stream))
+
+
+def sage_kv4_gather(cache, block_table, kv_lens, cu_seqlens, k_out, v_out, dtype, nseq, total, Hkv,
+                    rep, d, page_size, num_pages, max_pages, stream=None):
+    return _call("sage_kv4_gather", _ptr(cache), _ptr(block_table), _ptr(kv_lens),
+                 _ptr(cu_seqlens), _ptr(k_out), _ptr(v_out), dtype, nseq, total, Hkv, rep, d,
+                 page_size, num_pages, max_pages, _stream(stream))
+
+
+def sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) -> int:
+    return int(lib().sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d))
+
+
+def sage_attn_kv4(q, cache, block_table, kv_lens, cu_seqlens, out, lse, dtype, nseq, total, max_q,
+                  Hq, Hkv, d, page_size, num_pages, max_pages, causal, sm_scale, q_strides,
+                  workspace, ws_bytes, stream=None):
+    """q_strides: 2 integers or None (see sage.h)."""
+    return _call("sage_attn_kv4", _ptr(q), _ptr(cache), _ptr(block_table), _ptr(kv_lens),
+                 _ptr(cu_seqlens), _ptr(out), _ptr(lse), dtype, nseq, total, max_q, Hq, Hkv, d,
+                 page_size, num_pages, max_pages, int(causal), float(sm_scale), _i64s(q_strides),
+                 _ptr(workspace), ws_bytes, _stream(stream))
 
 
 def sage_attn_fwd_quantized_kv(q_i8, q_scale, k_i8, k_scale, v, v_scale, v_mean, q_comp, out, B,
@@ -505,6 +583,294 @@ def attn_decode(q_i8, q_scale, k_i8, k_scale, v, causal: bool = False, sm_scale:
     sage_attn_decode_quantized(q_i8, q_scale, k_i8, k_scale, v, out, B, H, Nq, Nk, d, causal,
                                sm_scale, SAGE_QK_FINE if fine else 0, workspace,
                                workspace.numel() * workspace.element_size(), stream)
+    return out
+
+
+# Rotary positions and the paged 4-bit cache. These wrappers take tensors as a model has them
+# (views of a fused projection included) and check shapes, types and devices, since a wrong one
+# would read or write elsewhere. A decode step makes these calls once per layer and its kernels
+# take a few microseconds, so a call's checks are one expression, and what to say about a wrong
+# argument is worked out only once one is wrong; the calls go straight to the library.
+
+ROPE_SCALINGS = {"plain": SAGE_ROPE_PLAIN, "linear": SAGE_ROPE_LINEAR, "base": SAGE_ROPE_BASE,
+                 "parts": SAGE_ROPE_PARTS}
+_PAGES = (16, 32, 64, 128, 256)
+_Strides2, _Strides8, _Strides12 = ctypes.c_int64 * 2, ctypes.c_int64 * 8, ctypes.c_int64 * 12
+_torch = None       # torch, its 16-bit types' codes, and what gives a device's current stream
+_half = {}
+_raw_stream = None
+
+
+def _setup():
+    global _torch, _raw_stream
+    import torch
+    _half.update({torch.float16: SAGE_F16, torch.bfloat16: SAGE_BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    lib()
+    return torch
+
+
+def _refuse(*wants):
+    """Raises for the first (tensor, what it has to be, whether it is) that is not."""
+    for x, what, ok in wants:
+        if not ok:
+            got = "None" if x is None else f"{str(x.dtype).replace('torch.', '')} {list(x.shape)} " \
+                f"with strides {list(x.stride())} on {x.device}"
+            raise ValueError(f"{what}, got {got}")
+    raise ValueError("the tensors' shapes, types and devices do not fit together")
+
+
+def _elsewhere(device: int) -> bool:
+    """Whether a device other than the tensors' (-1: the CPU's) is the current one."""
+    return device >= 0 and device != _torch.cuda.current_device()
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+               original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               device="cuda"):
+    """Angles per position of the rot_dim/2 rotated pairs (float64 tensor) and the factor on
+    cos and sin that belongs to them. scaling: "plain", "linear", "base" or "parts" (see
+    sage_rope_freqs in sage.h)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling is one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    freqs = torch.empty(max(rot_dim // 2, 0), dtype=torch.float64)
+    mscale = (ctypes.c_double * 1)()
+    sage_rope_freqs(freqs if rot_dim > 1 else None, mscale, rot_dim, base, ROPE_SCALINGS[scaling],
+                    factor, original_len, beta_fast, beta_slow)
+    return freqs.to(device), mscale[0]
+
+
+def rope(q, k, freqs, positions=None, mscale: float = 1.0, interleaved: bool = False,
+         inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [B, Hq, N, d] and k [B, Hk, N, d], or packed [T, H, d] (any
+    strides; k may be None): (q_out, k_out). freqs and mscale: rope_freqs. positions int32 [N],
+    [B, N] or [T]; None: 0 .. N-1. interleaved: pairs (2i, 2i+1), else (i, i + rot/2). inverse:
+    the rotation back, which is also its gradient. q_out=q, k_out=k rotates in place."""
+    torch = _torch or _setup()
+    dims, dev, dtype = q.dim(), q.get_device(), q.dtype
+    if dims == 3:
+        (N, Hq, d), B = q.shape, 1
+    elif dims == 4:
+        B, Hq, N, d = q.shape
+    else:
+        _refuse((q, "q is [B, H, N, d] or [T, H, d]", False))
+    Hk = 0 if k is None else k.shape[1] if k.dim() == dims else -1
+    kshape = (N, Hk, d) if dims == 3 else (B, Hk, N, d)
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    k_out = torch.empty_like(k) if k_out is None and k is not None else k_out
+    qs, qos = q.stride(), q_out.stride()
+    ks, kos = (k.stride(), k_out.stride()) if k is not None else (qs, qs)
+    code = _half.get(dtype)
+    if not (code is not None and qs[-1] == 1 == qos[-1] and q_out.shape == q.shape
+            and q_out.dtype == dtype and q_out.get_device() == dev
+            and (k is None or (k.shape == kshape and k_out.shape == kshape and ks[-1] == 1 == kos[-1]
+                               and k.dtype == dtype and k_out.dtype == dtype and k.get_device() == dev
+                               and k_out.get_device() == dev))
+            and freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous()
+            and freqs.get_device() == dev
+            and (positions is None or (positions.dtype == torch.int32 and positions.get_device() == dev
+                                       and positions.shape in ((N,), (B, N))
+                                       and (N < 2 or positions.stride(-1) == 1)))):
+        _refuse((q, "q is float16 or bfloat16 [B, H, N, d] or [T, H, d], its channels contiguous",
+                 code is not None and qs[-1] == 1),
+                (q_out, "q_out has q's shape, type and device", q_out.shape == q.shape
+                 and q_out.dtype == dtype and q_out.device == q.device and qos[-1] == 1),
+                (k, "k has q's type, device, tokens and head dim", k is None or (
+                    k.shape == kshape and k.dtype == dtype and k.device == q.device and ks[-1] == 1)),
+                (k_out, "k_out has k's shape, type and device", k is None or (
+                    k_out.shape == kshape and k_out.dtype == dtype and k_out.device == q.device and kos[-1] == 1)),
+                (freqs, "freqs is a contiguous float64 vector on q's device", freqs.dtype == torch.float64
+                 and freqs.dim() == 1 and freqs.is_contiguous() and freqs.device == q.device),
+                (positions, "positions is int32 [N], [B, N] or [T] on q's device", False))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return rope(q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out, stream)
+    if dims == 3:
+        strides = _Strides12(0, qs[1], qs[0], 0, qos[1], qos[0], 0, ks[1], ks[0], 0, kos[1], kos[0])
+    else:
+        strides = _Strides12(*qs[:3], *qos[:3], *ks[:3], *kos[:3])
+    rc = _lib.sage_rope(
+        q.data_ptr(), q_out.data_ptr(), None if k is None else k.data_ptr(),
+        None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
+        freqs.data_ptr(), code, B, N, Hq, Hk, d, 2 * freqs.shape[0],
+        positions.stride(0) if positions is not None and positions.dim() == 2 else 0, strides, mscale,
+        (SAGE_ROPE_INTERLEAVED if interleaved else 0) | (SAGE_ROPE_INVERSE if inverse else 0),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise SageError("sage_rope", rc)
+    return q_out, k_out
+
+
+def kv4_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):
+    """An empty paged 4-bit cache for head dim d: uint8 [num_pages, Hkv, page bytes]."""
+    import torch
+    n = sage_kv4_page_bytes(page_size, d)
+    if n == 0:
+        raise ValueError(f"page_size is a power of two from 16 to 256 and d is 64 or 128, got {page_size} and {d}")
+    return torch.empty((num_pages, Hkv, n), dtype=torch.uint8, device=device)
+
+
+def _kv4(cache, block_table, kv_lens, cu_seqlens, d: int):
+    """Checked sizes of a cache and its sequences: (nseq, Hkv, page_size, num_pages, max_pages, device)."""
+    torch = _torch or _setup()
+    i32, dev = torch.int32, cache.get_device()
+    num_pages, Hkv, page_bytes = cache.shape if cache.dim() == 3 else (0, 0, 0)
+    page_size = page_bytes * 8 // (9 * d) if d > 0 else 0
+    nseq = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    max_pages = block_table.shape[1] if block_table.dim() == 2 else -1
+    if not (page_size in _PAGES and page_size * 9 * d == page_bytes * 8 and cache.dtype == torch.uint8
+            and cache.is_contiguous() and nseq >= 0 and kv_lens.dtype == i32 and kv_lens.is_contiguous()
+            and kv_lens.get_device() == dev and block_table.shape == (nseq, max_pages)
+            and block_table.dtype == i32 and block_table.is_contiguous()
+            and block_table.get_device() == dev
+            and (cu_seqlens is None or (cu_seqlens.shape == (nseq + 1,) and cu_seqlens.dtype == i32
+                                        and cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev))):
+        fits = lambda x, shape: (x.dtype == i32 and x.is_contiguous() and x.device == cache.device  # noqa: E731
+                                 and tuple(x.shape) == shape)
+        _refuse((cache, "cache is a contiguous uint8 [num_pages, Hkv, page bytes] of kv4_cache for this head dim",
+                 page_size in _PAGES and page_size * 9 * d == page_bytes * 8
+                 and cache.dtype == torch.uint8 and cache.is_contiguous()),
+                (kv_lens, "kv_lens is contiguous int32 [nseq] on the cache's device", fits(kv_lens, (nseq,))),
+                (block_table, "block_table is contiguous int32 [nseq, max_pages] on the cache's device",
+                 fits(block_table, (nseq, max_pages))),
+                (cu_seqlens, "cu_seqlens is contiguous int32 [nseq + 1] on the cache's device", False))
+    return nseq, Hkv, page_size, num_pages, max_pages, dev
+
+
+def kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q=None, freqs=None,
+               mscale: float = 1.0, interleaved: bool = False, k_mean=None, q_out=None,
+               stream=None):
+    """Writes new tokens' k and v [T, Hkv, d] (any token and head strides) into the paged 4-bit
+    cache as the last tokens of their sequences, k rotated by their positions (freqs, mscale:
+    rope_freqs; None: not rotated) and lessened by k_mean [Hkv, d]; returns q [T, Hq, d] rotated
+    alike, or None. kv_lens int32 [nseq] counts the new tokens, cu_seqlens int32 [nseq+1] says
+    which rows are whose (None: T / nseq each), block_table int32 [nseq, max_pages] where the
+    pages are."""
+    torch = _torch or _setup()
+    T, Hkv, d = k.shape
+    nseq, heads, page_size, num_pages, max_pages, dev = _kv4(cache, block_table, kv_lens, cu_seqlens, d)
+    dtype, shape = k.dtype, k.shape
+    code = _half.get(dtype)
+    ks, vs = k.stride(), v.stride()
+    Hq, qs, qos, qp, qop = 0, ks, ks, None, None
+    q_ok = True
+    if q is not None:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        qs, qos, Hq = q.stride(), q_out.stride(), q.shape[1]
+        q_ok = (q.shape == (T, Hq, d) and q_out.shape == q.shape and q.dtype == dtype
+                and q_out.dtype == dtype and qs[2] == 1 == qos[2] and q.get_device() == dev
+                and q_out.get_device() == dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    if not (code is not None and heads == Hkv and v.shape == shape and v.dtype == dtype and q_ok
+            and ks[2] == 1 == vs[2] and k.get_device() == dev and v.get_device() == dev
+            and (freqs is None or (freqs.dtype == torch.float64 and freqs.dim() == 1
+                                   and freqs.is_contiguous() and freqs.get_device() == dev))
+            and (k_mean is None or (k_mean.dtype == torch.float32 and k_mean.shape == (Hkv, d)
+                                    and k_mean.is_contiguous() and k_mean.get_device() == dev))):
+        _refuse((k, "k is float16 or bfloat16 [T, Hkv, d] with the cache's heads and device, its channels contiguous",
+                 code is not None and heads == Hkv and ks[2] == 1 and k.device == cache.device),
+                (v, "v has k's shape, type and device", v.shape == shape and v.dtype == dtype
+                 and vs[2] == 1 and v.device == cache.device),
+                (q, "q is [T, Hq, d] of k's type and device, and q_out like it", q_ok),
+                (freqs, "freqs is a contiguous float64 vector on the cache's device", freqs is None or (
+                    freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous()
+                    and freqs.device == cache.device)),
+                (k_mean, "k_mean is a contiguous float32 [Hkv, d] on the cache's device", False))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q, freqs, mscale,
+                              interleaved, k_mean, q_out, stream)
+    rc = _lib.sage_kv4_append(
+        cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), qp, qop,
+        None if freqs is None else freqs.data_ptr(), None if k_mean is None else k_mean.data_ptr(), code,
+        nseq, T, Hq, Hkv, d, page_size, num_pages, max_pages, 0 if freqs is None else 2 * freqs.shape[0],
+        _Strides8(ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], qos[0], qos[1]), mscale,
+        SAGE_ROPE_INTERLEAVED if interleaved else 0,
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise SageError("sage_kv4_append", rc)
+    return q_out
+
+
+def kv4_gather(cache, block_table, kv_lens, cu_seqlens, total: int, d: int, dtype=None,
+               rep: int = 1, k_out=None, v_out=None, stream=None):
+    """The last cu_seqlens[s+1] - cu_seqlens[s] tokens of every sequence as 16-bit k and v
+    [total, Hkv * rep, d], each head rep times (dtype float16 by default): what
+    sageattn_varlen_kv takes for a prefill chunk over cached keys."""
+    torch = _torch or _setup()
+    nseq, Hkv, page_size, num_pages, max_pages, dev = _kv4(cache, block_table, kv_lens, cu_seqlens, d)
+    dtype = torch.float16 if dtype is None else dtype
+    shape = (total, Hkv * rep, d)
+    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+    v_out = torch.empty_like(k_out) if v_out is None else v_out
+    code = _half.get(dtype)
+    if not (code is not None and k_out.shape == shape and v_out.shape == shape and k_out.dtype == dtype
+            and v_out.dtype == dtype and k_out.is_contiguous() and v_out.is_contiguous()
+            and k_out.get_device() == dev and v_out.get_device() == dev):
+        fits = lambda x: (code is not None and x.shape == shape and x.dtype == dtype and x.is_contiguous()  # noqa: E731
+                          and x.device == cache.device)
+        what = f"contiguous {dtype} {list(shape)} on the cache's device, float16 or bfloat16"
+        _refuse((k_out, f"k_out is {what}", fits(k_out)), (v_out, f"v_out is {what}", fits(v_out)))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kv4_gather(cache, block_table, kv_lens, cu_seqlens, total, d, dtype, rep, k_out, v_out, stream)
+    rc = _lib.sage_kv4_gather(
+        cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), code,
+        nseq, total, Hkv, rep, d, page_size, num_pages, max_pages,
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise SageError("sage_kv4_gather", rc)
+    return k_out, v_out
+
+
+def attn_kv4(q, cache, block_table, kv_lens, cu_seqlens=None, max_q: Optional[int] = None,
+             causal: bool = True, sm_scale: float = 0.0, out=None, lse=None, workspace=None,
+             stream=None):
+    """Attention of q [T, Hq, d] (any token and head strides) over the paged 4-bit cache; query
+    head h reads key head h // (Hq / Hkv). A sequence has at most max_q queries (by default T /
+    nseq without cu_seqlens, else DECODE_MAX_Q), which are its last tokens. lse: float32 [T, Hq]
+    that takes the log of the softmax sums. The workspace is allocated here unless given."""
+    torch = _torch or _setup()
+    T, Hq, d = shape = q.shape
+    nseq, Hkv, page_size, num_pages, max_pages, dev = _kv4(cache, block_table, kv_lens, cu_seqlens, d)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    dtype, qs = q.dtype, q.stride()
+    code = _half.get(dtype)
+    if not (code is not None and qs[2] == 1 and q.get_device() == dev and out.shape == shape
+            and out.dtype == dtype and out.is_contiguous() and out.get_device() == dev
+            and (lse is None or (lse.dtype == torch.float32 and lse.shape == (T, Hq)
+                                 and lse.is_contiguous() and lse.get_device() == dev))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+        _refuse((q, "q is float16 or bfloat16 [T, Hq, d] on the cache's device, its channels contiguous",
+                 code is not None and qs[2] == 1 and q.device == cache.device),
+                (out, "out is contiguous and has q's shape, type and device", out.shape == shape
+                 and out.dtype == dtype and out.is_contiguous() and out.device == q.device),
+                (lse, "lse is a contiguous float32 [T, Hq] on q's device", lse is None or (
+                    lse.dtype == torch.float32 and lse.shape == (T, Hq) and lse.is_contiguous()
+                    and lse.device == q.device)),
+                (workspace, "workspace is contiguous and on q's device", False))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return attn_kv4(q, cache, block_table, kv_lens, cu_seqlens, max_q, causal, sm_scale, out, lse,
+                            workspace, stream)
+    if max_q is None:
+        max_q = DECODE_MAX_Q if cu_seqlens is not None else T // max(nseq, 1)
+    if workspace is None:
+        workspace = torch.empty(max(_lib.sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d), 16),
+                                dtype=torch.uint8, device=cache.device)
+    rc = _lib.sage_attn_kv4(
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), code, nseq, T, max_q, Hq, Hkv, d, page_size, num_pages,
+        max_pages, 1 if causal else 0, sm_scale, _Strides2(qs[0], qs[1]), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise SageError("sage_attn_kv4", rc)
     return out
 
 

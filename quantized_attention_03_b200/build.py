@@ -9,8 +9,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsage.so")
-SOURCES = ["api.cu", "quant.cu", "attn_sm100.cu", "decode.cu", "selftest.cu"]
-HEADERS = ["sage_common.cuh", "sm100_ptx.cuh", "quant_codes.cuh", "decode.cuh"]
+SOURCES = ["api.cu", "kv4_api.cu", "quant.cu", "attn_sm100.cu", "decode.cu", "rope.cu", "kv4.cu",
+           "kv4_attn.cu", "selftest.cu"]
+HEADERS = ["sage_common.cuh", "sm100_ptx.cuh", "quant_codes.cuh", "decode.cuh", "rope.cuh",
+           "kv4.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

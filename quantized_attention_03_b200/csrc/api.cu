@@ -22,6 +22,8 @@ int g_last_cuda_error = 0;
 std::mutex g_mu;
 int *g_status_ptr[64] = {};
 
+}  // namespace
+
 sage_status_t cuda_fail(cudaError_t e)
 {
     g_last_cuda_error = (int)e;
@@ -52,6 +54,8 @@ int *status_ptr(sage_status_t *err)
     *err = SAGE_OK;
     return g_status_ptr[dev];
 }
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -879,6 +883,7 @@ const char *sage_status_string(sage_status_t s)
     case SAGE_ERR_CUDA: return "SAGE_ERR_CUDA";
     case SAGE_ERR_TIMEOUT: return "SAGE_ERR_TIMEOUT";
     case SAGE_ERR_BAD_SEQLENS: return "SAGE_ERR_BAD_SEQLENS";
+    case SAGE_ERR_BAD_PAGE: return "SAGE_ERR_BAD_PAGE";
     }
     return "SAGE_ERR_UNKNOWN";
 }

@@ -1,0 +1,793 @@
+// Attention of a few queries per sequence over the paged 4-bit cache (format: kv4.cuh).
+//
+// For a query row q and a cached key k = low + step n (n the codes of a 64-channel group)
+//   t_j = sm_scale log2(e) (sum_g step_g (q_g . n_g) + low_g sum(q_g)),  p_j = 2^(t_j - m),
+//   O = sum_j p_j v_j / sum_j p_j,  v_j = (low' + step n'),  n' = n - 8, low' = low + 8 step,
+// so neither keys nor values are ever written out: the codes themselves are the operands of
+// two 16-bit tensor-core products and the params scale their 32-bit results (keys) or the
+// probabilities (values).
+//
+// What bounds it: the cache is read once from HBM, 0.5625 bytes per element, and each
+// element has to be turned from 4 bits into a 16-bit operand, so the instructions that
+// unpack (0.6 per key element, 1.3 per value element) are the second bound.
+//   - Keys: a code masked in place is an fp16 subnormal, n 2^-24 or 16 n 2^-24, which the
+//     tensor core multiplies exactly; one AND makes two operands. The queries of the second
+//     kind of channel are divided by 16 beforehand.
+//   - Values: codes are centred (n - 8), two operands per OR/AND and packed add, because the
+//     sum of p n' stays near the size of its result; uncentred it would be the difference of
+//     two sums 100 times larger, in which the accumulator's own rounding shows.
+//   - Probabilities times step are split into two fp16 terms, high and low, each with its own
+//     product: one term alone would round every p to 11 bits, as much error again as the
+//     rounding of the 16-bit output.
+// Queries are the 8-wide side of mma.m16n8k16 and keys (or channels) the 16-wide one, so a
+// group of up to 8 query rows that share a key head costs one pass; the 64-row or 128-row
+// tiles of tcgen05 would be almost empty here and could take the codes only from shared
+// memory, expanded to bytes.
+//
+// Work split: all (sequence, key head, row block, tile) of the call form one list, cut into
+// equal shares, one per CTA, whatever the sequences' lengths (which only the device knows);
+// the eight warps of a CTA take the share's tiles in turn, each through its own ring of
+// bulk copies, and are merged at the end of every (sequence, head). What a CTA began or
+// left unfinished goes to two partial slots of the workspace and a second kernel merges
+// those in order, so results do not depend on timing.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kv4.cuh"
+#include "rope.cuh"
+#include "sm100_ptx.cuh"
+
+namespace sage {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSMs = 148;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// D: head dim. NT: 8-row query tiles per pass (rows of one key head).
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kTile = 4096 / D;             // keys per warp tile
+    static constexpr int kGroups = D / kKv4Group;
+    static constexpr int kStages = NT == 1 ? 2 : 4;
+    static constexpr int kCtasPerSM = NT == 1 ? 2 : 1;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
+    static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
+    static constexpr int kPitch = D + 4;               // floats between rows of the merge buffer
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kSmem = kRing + kWarps * kRows * kPitch * 4;
+};
+
+// What a CTA that begins a (sequence, head, row block) and does not finish it leaves for the
+// merge: the last CTA that works on it (-1: nothing to merge) and whose rows they are.
+struct Tail {
+    int last, row0, n, kvh, rb;
+};
+
+struct Params {
+    Kv4AttnArgs a;
+    float *part;          // [ctas][2][rows][D + 2]: sums, then maximum and weight
+    Tail *tail;           // [ctas]
+    int group;            // query heads per key head
+    float sc_log2;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of 16-bit elements over the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t b) { return *reinterpret_cast<__half2 *>(&b); }
+
+// (x & mask) | 0x6400 in both halves: the fp16 number 1024 + code (or 1024 + 16 code).
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t biased(uint32_t x)
+{
+    return (x & kMask) | 0x64006400u;
+}
+
+// Tiles of a sequence: row blocks x key heads x key tiles; at least one tile where it has
+// queries, so that queries without keys are written too.
+template <int D, int NT>
+__device__ __forceinline__ int64_t sequence(const Params &p, int s, int &row0, int &n, int &len, int &nt, int &nrb)
+{
+    using C = Cfg<D, NT>;
+    int a, b;
+    nt = nrb = 0;
+    if (!p.a.s.rows(s, a, b, len))
+        return 0;
+    row0 = a;
+    n = b - a;
+    if (n == 0)
+        return 0;
+    if (n > p.a.max_q) {
+        atomicOr(p.a.s.status, status_bit(SAGE_ERR_BAD_SEQLENS));
+        return 0;
+    }
+    nt = max(1, (len + C::kTile - 1) / C::kTile);
+    nrb = (n * p.group + C::kRows - 1) / C::kRows;
+    return (int64_t)nt * nrb * p.a.s.Hkv;
+}
+
+// A walk over the segments (sequence, key head, row block, range of tiles) of a CTA's share
+// [x, x1) of the list.
+template <int D, int NT>
+struct Walk {
+    int64_t x, x1;
+    int s, row0, n, len, nt, nrb;     // the sequence
+    int kvh, rb, t0, t1;              // the segment
+
+    __device__ void start(const Params &p, int64_t from, int64_t to, int seq, int64_t offset)
+    {
+        x = from;
+        x1 = to;
+        s = seq;
+        sequence<D, NT>(p, s, row0, n, len, nt, nrb);
+        const int h = (int)(offset / nt);
+        t0 = (int)(offset % nt);
+        kvh = h / nrb;
+        rb = h % nrb;
+        t1 = (int)min((int64_t)nt, t0 + (x1 - x));
+    }
+    __device__ bool next(const Params &p)
+    {
+        x += t1 - t0;
+        if (x >= x1)
+            return false;
+        t0 = 0;
+        if (++rb == nrb) {
+            rb = 0;
+            if (++kvh == p.a.s.Hkv) {
+                kvh = 0;
+                do {
+                    if (++s >= p.a.s.nseq)
+                        return false;
+                } while (sequence<D, NT>(p, s, row0, n, len, nt, nrb) == 0);
+            }
+        }
+        t1 = (int)min((int64_t)nt, x1 - x);
+        return true;
+    }
+};
+
+__device__ __forceinline__ int64_t block_sum_scan(int64_t v, int64_t *s_warp, int64_t &total)
+{
+    // inclusive scan over the CTA
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += u;
+    }
+    __syncthreads();
+    if (lane == 31)
+        s_warp[warp] = v;
+    __syncthreads();
+    total = 0;
+    int64_t before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp)
+            before += s_warp[w];
+        total += s_warp[w];
+    }
+    return v + before;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_kernel(const Params p)
+{
+    using C = Cfg<D, NT>;
+    constexpr int kG = C::kGroups, kKB = C::kTile / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t s_bar[kWarps][C::kStages];
+    __shared__ int64_t s_scan[kWarps];
+    __shared__ int64_t s_from;
+    __shared__ int s_seq;
+    __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
+    __shared__ int s_abort;
+    float *s_o = reinterpret_cast<float *>(smem + C::kRing);
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
+    const int cta = blockIdx.x;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < C::kStages; i++)
+            mbar_init(&s_bar[warp][i], 1);
+        fence_barrier_init();
+    }
+    if (tid == 0)
+        s_abort = 0;
+    griddep_wait();
+
+    // ---- this CTA's share of the list
+    const Kv4Seqs &sq = p.a.s;
+    int row0, n, len, nt, nrb;
+    int64_t first = tid < sq.nseq ? sequence<D, NT>(p, tid, row0, n, len, nt, nrb) : 0;
+    int64_t total = 0, sum = 0;
+    for (int base = 0; base < sq.nseq; base += kThreads) {
+        int64_t v = first, all;
+        if (base)
+            v = base + tid < sq.nseq ? sequence<D, NT>(p, base + tid, row0, n, len, nt, nrb) : 0;
+        block_sum_scan(v, s_scan, all);
+        total += all;
+    }
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps));
+    const int64_t x0 = cta < ctas ? total * cta / ctas : total;
+    const int64_t x1 = cta < ctas ? total * (cta + 1) / ctas : total;
+    if (x0 >= x1) {
+        if (tid == 0)
+            p.tail[cta].last = -1;
+        return;
+    }
+    for (int base = 0; base < sq.nseq; base += kThreads) {
+        int64_t v = first, all;
+        if (base)
+            v = base + tid < sq.nseq ? sequence<D, NT>(p, base + tid, row0, n, len, nt, nrb) : 0;
+        const int64_t end = sum + block_sum_scan(v, s_scan, all);
+        if (end - v <= x0 && x0 < end) {
+            s_seq = base + tid;
+            s_from = end - v;
+        }
+        sum += all;
+    }
+    __syncthreads();
+    griddep_launch_dependents();
+
+    Walk<D, NT> seg, ahead;
+    seg.start(p, x0, x1, s_seq, x0 - s_from);
+    ahead = seg;
+
+    // ---- the warp's ring of tiles
+    uint8_t *ring = smem + warp * (C::kStages * C::kStageBytes);
+    const int ps = sq.page_size();
+    const int64_t page_bytes = kv4_page_bytes(ps, D);
+    const int slice = min(ps, C::kTile);               // keys per page of a tile
+    int next_tile = ahead.t0 + warp, issued = 0, used = 0;
+    bool more = true;
+    auto issue = [&]() {
+        while (more && next_tile >= ahead.t1) {
+            more = ahead.next(p);
+            next_tile = ahead.t0 + warp;
+        }
+        if (!more)
+            return;
+        const int k0 = next_tile * C::kTile;
+        const int rows = min(C::kTile, (ahead.len + 15) / 16 * 16 - k0);   // rows to fetch
+        const int cnt = min(slice, rows - lane * slice);                   // this lane's
+        int page = -1;
+        if (cnt > 0)
+            page = sq.page(ahead.s, k0 + lane * slice);
+        uint64_t *bar = &s_bar[warp][issued % C::kStages];
+        uint8_t *dst = ring + issued % C::kStages * C::kStageBytes;
+        const int bytes = page >= 0 ? cnt * (D + 8 * kG) : 0;
+        const int all = __reduce_add_sync(0xffffffffu, bytes);
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, all);
+        __syncwarp();
+        if (page >= 0) {
+            const int row = (k0 + lane * slice) & (ps - 1), at = lane * slice;
+            const uint8_t *src = sq.cache + ((int64_t)page * sq.Hkv + ahead.kvh) * page_bytes;
+            bulk_load_g2s(dst + at * (D / 2), src + row * (D / 2), cnt * (D / 2), bar);
+            bulk_load_g2s(dst + (C::kTile + at) * (D / 2), src + (ps + row) * (D / 2), cnt * (D / 2), bar);
+            bulk_load_g2s(dst + C::kTile * D + at * kG * 4, src + ps * D + row * kG * 4, cnt * kG * 4, bar);
+            bulk_load_g2s(dst + C::kTile * D + C::kParBytes + at * kG * 4,
+                          src + ps * D + (ps + row) * kG * 4, cnt * kG * 4, bar);
+        }
+        next_tile += kWarps;
+        issued++;
+    };
+#pragma unroll
+    for (int i = 0; i < C::kStages; i++)
+        issue();
+
+    int tail_last = -1;
+    Tail tail_info = {-1, 0, 0, 0, 0};
+    bool any = true;
+    while (any) {
+        // ---- the segment's queries: row r of the block is query r / group, head r % group
+        const int r0 = seg.rb * C::kRows, nrows = min(C::kRows, seg.n * p.group - r0);
+        uint32_t qf[NT][kG][2][4];
+        float f[NT][2], qs[NT][kG][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int nt8 = 0; nt8 < NT; nt8++) {
+            const int r = nt8 * 8 + g;
+            float x[kG][16];
+            float big = 0.0f;
+            const int qi = (r0 + r) / p.group, hh = (r0 + r) % p.group;
+            const int64_t off = (int64_t)(seg.row0 + qi) * p.a.q_tok +
+                                (int64_t)(seg.kvh * p.group + hh) * p.a.q_head + t4 * 16;
+#pragma unroll
+            for (int gr = 0; gr < kG; gr++) {
+                float lo8[8] = {}, hi8[8] = {};
+                if (r < nrows) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(p.a.q) + off + gr * 64);
+                    const uint4 u = __ldg(src), v = __ldg(src + 1);
+                    if (p.a.bf16) {
+                        load8<__nv_bfloat16>(u, lo8);
+                        load8<__nv_bfloat16>(v, hi8);
+                    } else {
+                        load8<__half>(u, lo8);
+                        load8<__half>(v, hi8);
+                    }
+                }
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    x[gr][i] = lo8[i];
+                    x[gr][8 + i] = hi8[i];
+                    s += lo8[i] + hi8[i];
+                    big = fmaxf(big, fmaxf(fabsf(lo8[i]), fabsf(hi8[i])));
+                }
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                s *= p.sc_log2;
+                qs[nt8][gr][0] = __shfl_sync(0xffffffffu, s, t4 * 8);
+                qs[nt8][gr][1] = __shfl_sync(0xffffffffu, s, t4 * 8 + 4);
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // the row as fp16 with its largest element in [2^14, 2^15): a factor 2^(14 - e)
+            const int e = max(-100, min(100, (int)(__float_as_uint(big) >> 23) - 127));
+            const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            const float back = __uint_as_float((uint32_t)(127 + 10 + e) << 23) * p.sc_log2;   // 2^(24 - 14 + e)
+            f[nt8][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
+            f[nt8][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+#pragma unroll
+            for (int gr = 0; gr < kG; gr++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const float *w = x[gr] + 8 * j;
+                    const float s16 = scale * 0.0625f;
+                    qf[nt8][gr][j][0] = pack_half2(w[0] * scale, w[4] * scale);
+                    qf[nt8][gr][j][1] = pack_half2(w[1] * s16, w[5] * s16);
+                    qf[nt8][gr][j][2] = pack_half2(w[2] * scale, w[6] * scale);
+                    qf[nt8][gr][j][3] = pack_half2(w[3] * s16, w[7] * s16);
+                }
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int rr = nt8 * 8 + 2 * t4 + c;
+                lim[nt8][c] = p.a.causal && rr < nrows ? seg.len - seg.n + (r0 + rr) / p.group : seg.len - 1;
+            }
+        }
+        // keys up to here are seen by every row of the block
+        const int seen = p.a.causal ? min(seg.len - 1, seg.len - seg.n + r0 / p.group) : seg.len - 1;
+
+        float m[NT][2], l[NT][2], o2[NT][kG][2], o[NT][kG][4][4];
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                m[i][c] = -INFINITY;
+                l[i][c] = 0.0f;
+            }
+#pragma unroll
+            for (int gr = 0; gr < kG; gr++) {
+                o2[i][gr][0] = o2[i][gr][1] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        o[i][gr][j][c] = 0.0f;
+            }
+        }
+        int vexp = -64;                                // exponent the value products are scaled for
+
+        for (int t = seg.t0 + warp; t < seg.t1; t += kWarps) {
+            const int k0 = t * C::kTile;
+            const uint8_t *st = ring + used % C::kStages * C::kStageBytes;
+            mbar_wait(&s_bar[warp][used % C::kStages], (used / C::kStages) & 1, &s_abort, sq.status,
+                      status_bit(SAGE_ERR_TIMEOUT), kTimeoutNs);
+            const bool masked = k0 + C::kTile - 1 > seen;
+
+            // ---- scores, S^T: rows are keys, columns query rows
+            float s[kKB][NT][4];
+            const __half2 *kpar = reinterpret_cast<const __half2 *>(st + C::kTile * D);
+#pragma unroll
+            for (int kb = 0; kb < kKB; kb++) {
+                const uint8_t *r0p = st + (kb * 16 + g) * (D / 2) + t4 * 8;
+                const uint8_t *r1p = r0p + 8 * (D / 2);
+                float add[NT][4];
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        s[kb][i][c] = add[i][c] = 0.0f;
+#pragma unroll
+                for (int gr = 0; gr < kG; gr++) {
+                    const uint2 w0 = *reinterpret_cast<const uint2 *>(r0p + gr * 32);
+                    const uint2 w1 = *reinterpret_cast<const uint2 *>(r1p + gr * 32);
+                    const float2 p0 = __half22float2(kpar[(kb * 16 + g) * kG + gr]);
+                    const float2 p1 = __half22float2(kpar[(kb * 16 + g + 8) * kG + gr]);
+                    float acc[NT][4] = {};
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        uint32_t u0 = j ? w0.y : w0.x, u1 = j ? w1.y : w1.x;
+#pragma unroll
+                        for (int hf = 0; hf < 2; hf++) {
+#pragma unroll
+                            for (int i = 0; i < NT; i++)
+                                mma16816(acc[i], u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u,
+                                         u1 & 0x00F000F0u, qf[i][gr][j][2 * hf], qf[i][gr][j][2 * hf + 1]);
+                            u0 >>= 8;
+                            u1 >>= 8;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; i++) {
+                        s[kb][i][0] = fmaf(p0.x, acc[i][0], s[kb][i][0]);
+                        s[kb][i][1] = fmaf(p0.x, acc[i][1], s[kb][i][1]);
+                        s[kb][i][2] = fmaf(p1.x, acc[i][2], s[kb][i][2]);
+                        s[kb][i][3] = fmaf(p1.x, acc[i][3], s[kb][i][3]);
+                        add[i][0] = fmaf(p0.y, qs[i][gr][0], add[i][0]);
+                        add[i][1] = fmaf(p0.y, qs[i][gr][1], add[i][1]);
+                        add[i][2] = fmaf(p1.y, qs[i][gr][0], add[i][2]);
+                        add[i][3] = fmaf(p1.y, qs[i][gr][1], add[i][3]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        s[kb][i][c] = fmaf(s[kb][i][c], f[i][c & 1], add[i][c]);
+            }
+            uint32_t hidden = 0;                       // of this lane's scores, bit kb*NT*4 + ...
+            if (masked) {
+#pragma unroll
+                for (int kb = 0; kb < kKB; kb++)
+#pragma unroll
+                    for (int i = 0; i < NT; i++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++)
+                            if (k0 + kb * 16 + g + (c >> 1) * 8 > lim[i][c & 1]) {
+                                s[kb][i][c] = -INFINITY;
+                                hidden |= 1u << ((kb * NT + i) * 4 + c);
+                            }
+            }
+
+            // ---- running maximum and the factor of what was summed before
+            float alpha[NT][2], base[NT][2];
+            bool move = false;
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    float x = -INFINITY;
+#pragma unroll
+                    for (int kb = 0; kb < kKB; kb++)
+                        x = fmaxf(x, fmaxf(s[kb][i][c], s[kb][i][c + 2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    x = fmaxf(x, m[i][c]);
+                    base[i][c] = x == -INFINITY ? 0.0f : x;
+                    alpha[i][c] = ex2_approx(m[i][c] - base[i][c]);
+                    move |= x != m[i][c];
+                    m[i][c] = x;
+                }
+            // ---- the tile's largest value step: the products p * step are scaled by a power of
+            // two that keeps them below 2^15 and the largest near 2^11, whatever V's size
+            const __half2 *vpar = reinterpret_cast<const __half2 *>(st + C::kTile * D + C::kParBytes);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < C::kTile * kG / 32; i++) {
+                const int e = lane + 32 * i;
+                const uint32_t b = reinterpret_cast<const uint32_t *>(vpar)[e] & 0xFFFFu;
+                if (k0 + e / kG < seg.len && b < 0x7C00u)
+                    top = max(top, b);
+            }
+            const int texp = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+            float shift = 1.0f;
+            if (texp > vexp + 3) {
+                shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
+                vexp = texp;
+                move = true;
+            }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        l[i][c] *= alpha[i][c];
+                        const float as = alpha[i][c] * shift;
+#pragma unroll
+                        for (int gr = 0; gr < kG; gr++) {
+                            o2[i][gr][c] *= alpha[i][c];
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                o[i][gr][j][c] *= as;
+                                o[i][gr][j][c + 2] *= as;
+                            }
+                        }
+                    }
+            }
+            const float vscale = __uint_as_float((uint32_t)(127 + 26 - vexp) << 23);
+
+            // ---- probabilities and O^T += V^T P^T: rows are channels, columns query rows
+#pragma unroll
+            for (int kb = 0; kb < kKB; kb++) {
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        s[kb][i][c] = ex2_approx(s[kb][i][c] - base[i][c & 1]);
+                        l[i][c & 1] += s[kb][i][c];
+                    }
+                const uint8_t *vr = st + (C::kTile + kb * 16 + 2 * t4) * (D / 2) + g * 4;
+#pragma unroll
+                for (int gr = 0; gr < kG; gr++) {
+                    const float2 p0 = __half22float2(vpar[(kb * 16 + g) * kG + gr]);
+                    const float2 p1 = __half22float2(vpar[(kb * 16 + g + 8) * kG + gr]);
+                    const float step0 = p0.x * vscale, step1 = p1.x * vscale;
+                    const float mid0 = fmaf(8.0f, p0.x, p0.y), mid1 = fmaf(8.0f, p1.x, p1.y);
+                    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+                    for (int i = 0; i < NT; i++) {
+                        float pv[4], pm[4];
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            pv[c] = s[kb][i][c] * (c < 2 ? step0 : step1);
+                            pm[c] = s[kb][i][c] * (c < 2 ? mid0 : mid1);
+                        }
+                        if (masked) {                  // 0 times what lies in a hidden place is 0
+#pragma unroll
+                            for (int c = 0; c < 4; c++)
+                                if (hidden >> ((kb * NT + i) * 4 + c) & 1)
+                                    pv[c] = pm[c] = 0.0f;
+                        }
+                        o2[i][gr][0] += pm[0] + pm[2];
+                        o2[i][gr][1] += pm[1] + pm[3];
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const __half2 a = __floats2half2_rn(pv[2 * h], pv[2 * h + 1]);
+                            const float2 b = __half22float2(a);
+                            hi[i][h] = transpose8x8(h2_bits(a));
+                            lo[i][h] = transpose8x8(pack_half2(pv[2 * h] - b.x, pv[2 * h + 1] - b.y));
+                        }
+                    }
+                    // keys 2t, 2t+1 (A, B) and 2t+8, 2t+9 (C, D) of the block; 8 channels each
+                    const uint32_t wa = *reinterpret_cast<const uint32_t *>(vr + gr * 32);
+                    const uint32_t wb = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + D / 2);
+                    const uint32_t wc = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 8 * (D / 2));
+                    const uint32_t wd = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 9 * (D / 2));
+                    const __half2 sub = bits_h2(0xE408E408u);         // -1032
+                    const __half2 sixteenth = bits_h2(0x2C002C00u);   // 1 / 16
+                    const __half2 sub16 = bits_h2(0xD480D480u);       // -72
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {      // channels 0-3, then 4-7 of the word
+                        uint32_t ab = __byte_perm(wa, wb, q ? 0x7632 : 0x5410);
+                        uint32_t cd = __byte_perm(wc, wd, q ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const uint32_t a0 = h2_bits(__hadd2(bits_h2(biased<0x000F000Fu>(ab)), sub));
+                            const uint32_t a1 = h2_bits(__hfma2(bits_h2(biased<0x00F000F0u>(ab)), sixteenth, sub16));
+                            const uint32_t a2 = h2_bits(__hadd2(bits_h2(biased<0x000F000Fu>(cd)), sub));
+                            const uint32_t a3 = h2_bits(__hfma2(bits_h2(biased<0x00F000F0u>(cd)), sixteenth, sub16));
+#pragma unroll
+                            for (int i = 0; i < NT; i++) {
+                                mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, hi[i][0], hi[i][1]);
+                                mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, lo[i][0], lo[i][1]);
+                            }
+                            ab >>= 8;
+                            cd >>= 8;
+                        }
+                    }
+                }
+            }
+            __syncwarp();                              // the stage is read
+            used++;
+            issue();
+        }
+
+        // ---- merge the warps: maximum, weight and sums of each row through shared memory
+        const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 - 26 + vexp) << 23);
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int r = i * 8 + 2 * t4 + c;
+                float lw = l[i][c], ow[kG];
+#pragma unroll
+                for (int gr = 0; gr < kG; gr++)
+                    ow[gr] = o2[i][gr][c];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    lw += __shfl_xor_sync(0xffffffffu, lw, x);
+#pragma unroll
+                    for (int gr = 0; gr < kG; gr++)
+                        ow[gr] += __shfl_xor_sync(0xffffffffu, ow[gr], x);
+                }
+                if (g == 0) {
+                    s_m[warp][r] = m[i][c];
+                    s_l[warp][r] = lw;
+                }
+                if (r < nrows) {
+                    float *dst = s_o + (warp * C::kRows + r) * C::kPitch + g * 8;
+#pragma unroll
+                    for (int gr = 0; gr < kG; gr++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            *reinterpret_cast<float2 *>(dst + gr * 64 + 2 * j) =
+                                make_float2(fmaf(o[i][gr][j][c], unscale, ow[gr]),
+                                            fmaf(o[i][gr][j][c + 2], unscale, ow[gr]));
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
+        for (int e = tid; e < nrows * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), c4 = e % (D / 4) * 4;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++)
+                M = fmaxf(M, s_m[w][r]);
+            const float b = M == -INFINITY ? 0.0f : M;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float wt = ex2_approx(s_m[w][r] - b);
+                const float4 v = *reinterpret_cast<const float4 *>(s_o + (w * C::kRows + r) * C::kPitch + c4);
+                L = fmaf(wt, s_l[w][r], L);
+                acc.x = fmaf(wt, v.x, acc.x);
+                acc.y = fmaf(wt, v.y, acc.y);
+                acc.z = fmaf(wt, v.z, acc.z);
+                acc.w = fmaf(wt, v.w, acc.w);
+            }
+            if (whole) {
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                const int64_t row = seg.row0 + (r0 + r) / p.group;
+                const int head = seg.kvh * p.group + (r0 + r) % p.group;
+                const int64_t at = (row * p.a.Hq + head) * D + c4;
+                uint2 u;
+                if (p.a.bf16) {
+                    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+                    h[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                    h[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                } else {
+                    u.x = pack_half2(acc.x * inv, acc.y * inv);
+                    u.y = pack_half2(acc.z * inv, acc.w * inv);
+                }
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + at) = u;
+                if (c4 == 0 && p.a.lse)
+                    p.a.lse[row * p.a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+            } else {
+                float *part = p.part + ((int64_t)(cta * 2 + (seg.t0 == 0)) * C::kRows + r) * (D + 2);
+                *reinterpret_cast<float2 *>(part + c4) = make_float2(acc.x, acc.y);
+                *reinterpret_cast<float2 *>(part + c4 + 2) = make_float2(acc.z, acc.w);
+                if (c4 == 0) {
+                    part[D] = M;
+                    part[D + 1] = L;
+                }
+            }
+        }
+        if (!whole && seg.t0 == 0) {
+            // the list's position behind the segment's last tile lies in the share of CTA
+            // ceil(end ctas / total) - 1
+            const int64_t end = seg.x + seg.nt;
+            tail_info = Tail{(int)((end * ctas + total - 1) / total) - 1, seg.row0, seg.n, seg.kvh, seg.rb};
+            tail_last = tail_info.last;
+        }
+        any = seg.next(p);
+        __syncthreads();                               // the merge buffer is free again
+    }
+    // a wait that gave up: let this warp's own copies land before the CTA's memory is reused
+    if (s_abort)
+        for (; used < issued; used++)
+            mbar_wait(&s_bar[warp][used % C::kStages], (used / C::kStages) & 1, nullptr, sq.status,
+                      status_bit(SAGE_ERR_TIMEOUT), kTimeoutNs);
+    if (tid == 0) {
+        tail_info.last = tail_last;
+        p.tail[cta] = tail_info;
+    }
+}
+
+// Merge of what several CTAs share: CTA (c, r) takes row r of the segment that CTA c began.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) kv4_attn_merge(const Params p)
+{
+    using C = Cfg<D, NT>;
+    griddep_wait();
+    const int c0 = blockIdx.x, r = blockIdx.y, ch = threadIdx.x;
+    const Tail t = p.tail[c0];
+    const int rr = t.rb * C::kRows + r;
+    if (t.last < 0 || rr >= t.n * p.group)
+        return;
+    auto slot = [&](int c) {
+        return p.part + ((int64_t)(c * 2 + (c == c0)) * C::kRows + r) * (D + 2);
+    };
+    float M = -INFINITY;
+    for (int c = c0; c <= t.last; c++)
+        M = fmaxf(M, slot(c)[D]);
+    const float b = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f, O = 0.0f;
+    for (int c = c0; c <= t.last; c++) {
+        const float *s = slot(c);
+        const float w = ex2_approx(s[D] - b);
+        L = fmaf(w, s[D + 1], L);
+        O = fmaf(w, s[ch], O);
+    }
+    const int64_t row = t.row0 + rr / p.group;
+    const int head = t.kvh * p.group + rr % p.group;
+    const int64_t at = (row * p.a.Hq + head) * D + ch;
+    const float v = L == 0.0f ? 0.0f : O / L;
+    if (p.a.bf16)
+        static_cast<__nv_bfloat16 *>(p.a.out)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(p.a.out)[at] = __float2half_rn(v);
+    if (ch == 0 && p.a.lse)
+        p.a.lse[row * p.a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// Rows of a pass: 8 where the queries of a key head fit, else 16.
+int query_tiles(int Hq, int Hkv, int max_q) { return max_q * (Hq / Hkv) <= 8 ? 1 : 2; }
+int ctas(int nt) { return nt == 1 ? 2 * kSMs : kSMs; }
+
+template <int D, int NT>
+cudaError_t launch(const Params &p, cudaStream_t st)
+{
+    using C = Cfg<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    kv4_attn_kernel<D, NT><<<ctas(NT), kThreads, C::kSmem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    const int rows = std::min(C::kRows, p.a.max_q * p.group);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas(NT), rows);
+    cfg.blockDim = dim3(D);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_attn_merge<D, NT>, p);
+}
+
+size_t tail_bytes(int nt) { return (sizeof(Tail) * ctas(nt) + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t kv4_attn_workspace(int Hq, int Hkv, int max_q, int d)
+{
+    const int nt = query_tiles(Hq, Hkv, max_q);
+    return tail_bytes(nt) + (size_t)ctas(nt) * 2 * 8 * nt * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t st)
+{
+    const int nt = query_tiles(a.Hq, a.s.Hkv, a.max_q);
+    Params p;
+    p.a = a;
+    p.tail = static_cast<Tail *>(a.workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + tail_bytes(nt));
+    p.group = a.Hq / a.s.Hkv;
+    p.sc_log2 = a.sm_scale * kLog2e;
+    if (a.d == 128)
+        return nt == 1 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
+    return nt == 1 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
+}
+
+}  // namespace sage

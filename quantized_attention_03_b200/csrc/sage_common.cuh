@@ -139,4 +139,9 @@ cudaError_t launch_attention(const AttnArgs &a, const SeqLayout &Lq, const SeqLa
                              int *status, cudaStream_t st, sage_status_t *host_err);
 cudaError_t launch_wait_selftest(int *status, uint64_t timeout_ns, cudaStream_t st);
 
+// Host helpers of the C-ABI layer (api.cu): the current device's status word (nullptr and
+// *err on failure), and the status code of a failed CUDA call.
+int *status_ptr(sage_status_t *err);
+sage_status_t cuda_fail(cudaError_t e);
+
 }  // namespace sage

@@ -1,0 +1,213 @@
+"""Rotary positions and the 4-bit cache without a GPU: the angles' formulas, and every refusal
+of the C entry points and of the wrappers, all of which happen before any CUDA call."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import quantized_attention_03_b200 as sage
+
+FAKE, MIS = 0x10000, 0x10008      # 16-byte aligned, and not; never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from quantized_attention_03_b200 import build
+    build.build()
+    return sage.lib()
+
+
+# ---------------------------------------------------------------------------- angles
+
+
+@pytest.mark.parametrize("rot,base", [(16, 10000.0), (64, 10000.0), (128, 500000.0), (2, 100.0)])
+def test_plain_and_linear_freqs(lib, rot, base):
+    f, m = sage.rope_freqs(rot, base, device="cpu")
+    assert m == 1.0 and f.shape == (rot // 2,)
+    for i in range(rot // 2):
+        assert f[i].item() == pytest.approx(math.exp(-2 * i / rot * math.log(base)), rel=1e-14)
+    g, m = sage.rope_freqs(rot, base, "linear", 4.0, device="cpu")
+    assert m == 1.0 and torch.equal(g, f / 4)
+
+
+def test_base_scaling_keeps_the_fastest_pair_and_divides_the_slowest(lib):
+    f, _ = sage.rope_freqs(128, device="cpu")
+    g, m = sage.rope_freqs(128, scaling="base", factor=8.0, device="cpu")
+    assert m == 1.0 and g[0] == f[0]
+    assert g[-1].item() == pytest.approx(f[-1].item() / 8, rel=1e-12)
+    assert bool((g[1:] < f[1:]).all())
+
+
+def test_parts_scaling(lib):
+    f, _ = sage.rope_freqs(128, device="cpu")
+    g, m = sage.rope_freqs(128, scaling="parts", factor=16.0, original_len=4096, device="cpu")
+    assert m == pytest.approx(0.1 * math.log(16) + 1, rel=1e-15)
+    turns = 4096 * f / (2 * math.pi)
+    share = (1 - g / f) / (1 - 1 / 16)                # 0: kept, 1: divided by the factor
+    assert bool((share[turns > 33] < 0.03).all()) and bool((share[turns < 0.95] > 0.97).all())
+    assert bool((share.diff() >= -1e-12).all())
+    mid = (turns < 25) & (turns > 1.5)
+    assert bool((share[mid] > 0.02).all()) and bool((share[mid] < 0.99).all())
+    same, m = sage.rope_freqs(128, scaling="parts", factor=1.0, original_len=4096, device="cpu")
+    assert m == 1.0 and torch.allclose(same, f, rtol=1e-15, atol=0)
+
+
+def test_freqs_refusals(lib):
+    out = (ctypes.c_double * 64)()
+
+    def go(freqs=out, rot=128, base=1e4, scaling=0, factor=2.0, orig=4096.0, fast=32.0, slow=1.0):
+        return lib.sage_rope_freqs(freqs, None, rot, base, scaling, factor, orig, fast, slow)
+
+    bad = sage.SAGE_ERR_INVALID_ARG
+    assert go() == sage.SAGE_OK
+    assert go(freqs=None) == bad and go(rot=0) == bad and go(rot=7) == bad and go(rot=-2) == bad
+    assert go(base=1.0) == bad and go(base=math.nan) == bad
+    assert go(scaling=4) == bad and go(scaling=-1) == bad
+    assert go(scaling=1, factor=0.5) == bad and go(scaling=2, rot=2) == bad
+    assert go(scaling=3, orig=0.0) == bad and go(scaling=3, fast=1.0) == bad
+    assert go(scaling=3, slow=0.0) == bad
+    with pytest.raises(ValueError):
+        sage.rope_freqs(64, scaling="other", device="cpu")
+    with pytest.raises(sage.SageError):
+        sage.rope_freqs(0, device="cpu")
+
+
+# -------------------------------------------------------------------- C entry points
+
+
+def _rope(lib, q=FAKE, qo=FAKE, k=FAKE, ko=FAKE, freqs=FAKE, dtype=0, B=1, N=4, Hq=2, Hk=2, d=128, rot=128,
+          strides=None, flags=0):
+    s = None if strides is None else (ctypes.c_int64 * 12)(*strides)
+    return lib.sage_rope(q, qo, k, ko, None, freqs, dtype, B, N, Hq, Hk, d, rot, 0, s, 1.0, flags, None)
+
+
+def test_rope_refusals(lib):
+    bad, uns, mis = sage.SAGE_ERR_INVALID_ARG, sage.SAGE_ERR_UNSUPPORTED, sage.SAGE_ERR_MISALIGNED
+    assert _rope(lib, q=0) == bad and _rope(lib, qo=0) == bad and _rope(lib, k=0) == bad and _rope(lib, ko=0) == bad
+    assert _rope(lib, freqs=0) == bad and _rope(lib, dtype=2) == bad and _rope(lib, B=-1) == bad
+    assert _rope(lib, rot=0) == bad and _rope(lib, rot=144) == bad and _rope(lib, rot=-16) == bad
+    assert _rope(lib, rot=24) == uns and _rope(lib, d=96, rot=32) == uns and _rope(lib, Hq=70000) == uns
+    assert _rope(lib, B=65536, N=65536) == uns
+    assert _rope(lib, flags=4) == bad
+    assert _rope(lib, q=MIS) == mis and _rope(lib, ko=MIS) == mis
+    assert _rope(lib, strides=[512, 256, 130] + [512, 256, 128] * 3) == mis
+    assert _rope(lib, B=0) == sage.SAGE_OK and _rope(lib, N=0, q=0) == sage.SAGE_OK
+    assert _rope(lib, Hq=0, Hk=0) == sage.SAGE_OK
+
+
+def _append(lib, cache=FAKE, table=FAKE, lens=FAKE, cu=FAKE, k=FAKE, v=FAKE, q=FAKE, qo=FAKE, freqs=FAKE, mean=None,
+            dtype=0, nseq=2, total=4, Hq=4, Hkv=2, d=128, page=16, pages=8, width=4, rot=128, strides=None, flags=0):
+    s = None if strides is None else (ctypes.c_int64 * 8)(*strides)
+    return lib.sage_kv4_append(cache, table, lens, cu, k, v, q, qo, freqs, mean, dtype, nseq, total, Hq, Hkv, d, page,
+                               pages, width, rot, s, 1.0, flags, None)
+
+
+def test_append_refusals(lib):
+    bad, uns, mis = sage.SAGE_ERR_INVALID_ARG, sage.SAGE_ERR_UNSUPPORTED, sage.SAGE_ERR_MISALIGNED
+    for name in ("cache", "table", "lens", "k", "v", "qo", "freqs"):
+        assert _append(lib, **{name: 0}) == bad, name
+    for name in ("dtype", "nseq", "total", "Hkv", "pages", "width", "Hq"):
+        assert _append(lib, **{name: -1}) == bad, name
+    for page in (0, 8, 24, 512, -16):
+        assert _append(lib, page=page) == uns, page
+    assert _append(lib, d=96) == uns and _append(lib, rot=40) == uns and _append(lib, rot=256) == bad
+    assert _append(lib, flags=sage.SAGE_ROPE_INVERSE) == bad
+    assert _append(lib, cu=0, total=5) == bad          # 5 rows do not divide into 2 sequences
+    for name in ("cache", "k", "v", "q", "qo", "mean"):
+        assert _append(lib, **{name: MIS}) == mis, name
+    assert _append(lib, strides=[256, 128, 256, 132, 512, 128, 512, 128]) == mis
+    assert _append(lib, nseq=0) == sage.SAGE_OK and _append(lib, total=0, cache=0) == sage.SAGE_OK
+
+
+def _gather(lib, cache=FAKE, table=FAKE, lens=FAKE, cu=FAKE, ko=FAKE, vo=FAKE, dtype=0, nseq=2, total=4, Hkv=2, rep=1,
+            d=128, page=16, pages=8, width=4):
+    return lib.sage_kv4_gather(cache, table, lens, cu, ko, vo, dtype, nseq, total, Hkv, rep, d, page, pages, width, None)
+
+
+def test_gather_refusals(lib):
+    bad, uns, mis = sage.SAGE_ERR_INVALID_ARG, sage.SAGE_ERR_UNSUPPORTED, sage.SAGE_ERR_MISALIGNED
+    for name in ("cache", "table", "lens", "ko", "vo", "rep"):
+        assert _gather(lib, **{name: 0}) == bad, name
+    assert _gather(lib, dtype=5) == bad and _gather(lib, page=17) == uns and _gather(lib, d=80) == uns
+    for name in ("cache", "ko", "vo"):
+        assert _gather(lib, **{name: MIS}) == mis, name
+    assert _gather(lib, total=0, ko=0) == sage.SAGE_OK
+
+
+def _attn(lib, q=FAKE, cache=FAKE, table=FAKE, lens=FAKE, cu=FAKE, out=FAKE, lse=None, dtype=0, nseq=2, total=4,
+          max_q=2, Hq=4, Hkv=2, d=128, page=16, pages=8, width=4, strides=None, ws=FAKE, ws_bytes=1 << 30):
+    s = None if strides is None else (ctypes.c_int64 * 2)(*strides)
+    return lib.sage_attn_kv4(q, cache, table, lens, cu, out, lse, dtype, nseq, total, max_q, Hq, Hkv, d, page, pages,
+                             width, 1, 0.0, s, ws, ws_bytes, None)
+
+
+def test_attn_refusals(lib):
+    bad, uns, mis = sage.SAGE_ERR_INVALID_ARG, sage.SAGE_ERR_UNSUPPORTED, sage.SAGE_ERR_MISALIGNED
+    for name in ("q", "cache", "table", "lens", "out", "ws", "max_q"):
+        assert _attn(lib, **{name: 0}) == bad, name
+    assert _attn(lib, Hq=5) == bad and _attn(lib, Hkv=0) == bad and _attn(lib, max_q=-1) == bad
+    assert _attn(lib, max_q=17) == uns and _attn(lib, page=12) == uns and _attn(lib, d=32) == uns
+    assert _attn(lib, cu=0, max_q=1) == bad            # 4 rows of 2 sequences: two queries each
+    for name in ("q", "cache", "out", "ws"):
+        assert _attn(lib, **{name: MIS}) == mis, name
+    assert _attn(lib, strides=[512, 100]) == mis
+    need = lib.sage_attn_kv4_workspace_size(4, 2, 2, 128)
+    assert need > 0 and _attn(lib, ws_bytes=need - 1) == sage.SAGE_ERR_WORKSPACE
+    assert _attn(lib, total=0, q=0) == sage.SAGE_OK and _attn(lib, nseq=0) == sage.SAGE_OK
+
+
+def test_sizes(lib):
+    assert sage.sage_kv4_page_bytes(16, 64) == 16 * 64 // 2 * 2 + 16 * 4 * 2
+    assert sage.sage_kv4_page_bytes(256, 128) == 256 * (128 + 16)
+    for page, d in ((15, 64), (512, 64), (16, 96), (0, 128), (-16, 64)):
+        assert sage.sage_kv4_page_bytes(page, d) == 0
+    size = sage.sage_attn_kv4_workspace_size
+    assert size(32, 8, 1, 128) > 0 and size(32, 8, 17, 128) == 0 and size(32, 5, 1, 128) == 0
+    assert size(0, 0, 1, 128) == 0 and size(8, 8, 1, 96) == 0
+
+
+# -------------------------------------------------------------------------- wrappers
+
+
+def _cpu_sequences(nseq=2, width=2, pages=4, Hkv=2, d=64, page=16):
+    cache = sage.kv4_cache(pages, Hkv, page, d, device="cpu")
+    table = torch.zeros((nseq, width), dtype=torch.int32)
+    return cache, table, torch.ones(nseq, dtype=torch.int32), torch.arange(nseq + 1, dtype=torch.int32)
+
+
+def test_wrappers_refuse_wrong_tensors_before_the_library(lib):
+    cache, table, lens, cu = _cpu_sequences()
+    f, _ = sage.rope_freqs(64, device="cpu")
+    k = torch.zeros((2, 2, 64), dtype=torch.float16)
+    q = torch.zeros((2, 4, 64), dtype=torch.float16)
+    wrong = [
+        lambda: sage.kv4_append(cache, table, lens, cu, k[:, :1], k, q, f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k.bfloat16(), q, f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k.float(), k.float(), None, f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q[:1], f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q, f.float()),
+        lambda: sage.kv4_append(cache, table.long(), lens, cu, k, k, q, f),
+        lambda: sage.kv4_append(cache, table, lens, cu[:-1], k, k, q, f),
+        lambda: sage.kv4_append(cache, table[:1], lens, cu, k, k, q, f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q, f, k_mean=torch.zeros(2, 32)),
+        lambda: sage.kv4_append(cache[..., :-9], table, lens, cu, k, k, q, f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q, f, q_out=q.bfloat16()),
+        lambda: sage.kv4_gather(cache, table, lens, cu, 2, 128),
+        lambda: sage.kv4_gather(cache, table, lens, cu, 2, 64, dtype=torch.float32),
+        lambda: sage.kv4_gather(cache, table, lens, cu, 2, 64, k_out=torch.zeros((2, 4, 64), dtype=torch.float16)),
+        lambda: sage.attn_kv4(q, cache, table, lens, cu, 1, out=q.transpose(0, 1)),
+        lambda: sage.attn_kv4(q, cache, table, lens, cu, 1, lse=torch.zeros(2, 4).double()),
+        lambda: sage.attn_kv4(q.float(), cache, table, lens, cu, 1),
+        lambda: sage.attn_kv4(torch.zeros((2, 4, 128), dtype=torch.float16), cache, table, lens, cu, 1),
+        lambda: sage.rope(q, k[:1], f),
+        lambda: sage.rope(q, k, f, torch.zeros(2, dtype=torch.int64)),
+        lambda: sage.rope(q, k, f, torch.zeros(3, dtype=torch.int32)),
+        lambda: sage.rope(q[0], None, f),
+        lambda: sage.rope(q.transpose(1, 2), None, f),
+        lambda: sage.kv4_cache(4, 2, 20, 64, device="cpu"),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(i)
