@@ -42,7 +42,7 @@ sage_status_t check_seqs(int dtype, int nseq, int total, int Hkv, int d, int pag
         return SAGE_ERR_UNSUPPORTED;
     if (page_size < kKv4MinPage || page_size > kKv4MaxPage || (page_size & (page_size - 1)))
         return SAGE_ERR_UNSUPPORTED;
-    if (!cu_seqlens && nseq > 0 && total % nseq)
+    if ((!cu_seqlens && nseq > 0 && total % nseq) || (num_pages == 0 && nseq > 0 && total > 0))
         return SAGE_ERR_INVALID_ARG;
     return SAGE_OK;
 }

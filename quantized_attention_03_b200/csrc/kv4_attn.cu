@@ -27,7 +27,7 @@
 // Work split: all (sequence, key head, row block, tile) of the call form one list, cut into
 // equal shares, one per CTA, whatever the sequences' lengths (which only the device knows);
 // the eight warps of a CTA take the share's tiles in turn, each through its own ring of
-// bulk copies, and are merged at the end of every (sequence, head). What a CTA began or
+// copies, and are merged at the end of every (sequence, head). What a CTA began or
 // left unfinished goes to two partial slots of the workspace and a second kernel merges
 // those in order, so results do not depend on timing.
 #include <math.h>
@@ -44,18 +44,19 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSMs = 148;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// D: head dim. NT: 8-row query tiles per pass (rows of one key head).
-template <int D, int NT>
+// D: head dim. NT: 8-row query tiles per pass (rows of one key head). FOLD (NT = 1): at most 4
+// rows, twice in the tile: the high terms of P in columns 0-3 and the low ones in 4-7, so that
+// one value product takes both.
+template <int D, int NT, bool FOLD>
 struct Cfg {
     static constexpr int kTile = 4096 / D;             // keys per warp tile
     static constexpr int kGroups = D / kKv4Group;
     static constexpr int kStages = NT == 1 ? 2 : 4;
     static constexpr int kCtasPerSM = NT == 1 ? 2 : 1;
-    static constexpr int kRows = 8 * NT;
+    static constexpr int kRows = FOLD ? 4 : 8 * NT;
     static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
     static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
     static constexpr int kPitch = D + 4;               // floats between rows of the merge buffer
@@ -96,19 +97,40 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t b) { return *reinterpret_cast<__half2 *>(&b); }
 
+// 16-byte asynchronous copy, global to shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // (x & mask) | 0x6400 in both halves: the fp16 number 1024 + code (or 1024 + 16 code).
 template <uint32_t kMask>
 __device__ __forceinline__ uint32_t biased(uint32_t x)
 {
-    return (x & kMask) | 0x64006400u;
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(kMask), "r"(0x64006400u));
+    return r;
+}
+
+// (step, low) of a key's or value's groups.
+template <int G>
+__device__ __forceinline__ void load_params(const uint32_t *at, float2 (&p)[G])
+{
+    if constexpr (G == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(at);
+        p[0] = __half22float2(bits_h2(u.x));
+        p[1] = __half22float2(bits_h2(u.y));
+    } else {
+        p[0] = __half22float2(bits_h2(*at));
+    }
 }
 
 // Tiles of a sequence: row blocks x key heads x key tiles; at least one tile where it has
 // queries, so that queries without keys are written too.
-template <int D, int NT>
+template <int D, int NT, bool FOLD>
 __device__ __forceinline__ int64_t sequence(const Params &p, int s, int &row0, int &n, int &len, int &nt, int &nrb)
 {
-    using C = Cfg<D, NT>;
+    using C = Cfg<D, NT, FOLD>;
     int a, b;
     nt = nrb = 0;
     if (!p.a.s.rows(s, a, b, len))
@@ -128,7 +150,7 @@ __device__ __forceinline__ int64_t sequence(const Params &p, int s, int &row0, i
 
 // A walk over the segments (sequence, key head, row block, range of tiles) of a CTA's share
 // [x, x1) of the list.
-template <int D, int NT>
+template <int D, int NT, bool FOLD>
 struct Walk {
     int64_t x, x1;
     int s, row0, n, len, nt, nrb;     // the sequence
@@ -139,7 +161,7 @@ struct Walk {
         x = from;
         x1 = to;
         s = seq;
-        sequence<D, NT>(p, s, row0, n, len, nt, nrb);
+        sequence<D, NT, FOLD>(p, s, row0, n, len, nt, nrb);
         const int h = (int)(offset / nt);
         t0 = (int)(offset % nt);
         kvh = h / nrb;
@@ -159,7 +181,7 @@ struct Walk {
                 do {
                     if (++s >= p.a.s.nseq)
                         return false;
-                } while (sequence<D, NT>(p, s, row0, n, len, nt, nrb) == 0);
+                } while (sequence<D, NT, FOLD>(p, s, row0, n, len, nt, nrb) == 0);
             }
         }
         t1 = (int)min((int64_t)nt, x1 - x);
@@ -192,41 +214,31 @@ __device__ __forceinline__ int64_t block_sum_scan(int64_t v, int64_t *s_warp, in
     return v + before;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_kernel(const Params p)
+template <int D, int NT, bool FOLD>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_attn_kernel(const Params p)
 {
-    using C = Cfg<D, NT>;
+    using C = Cfg<D, NT, FOLD>;
     constexpr int kG = C::kGroups, kKB = C::kTile / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t s_bar[kWarps][C::kStages];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int64_t s_from;
     __shared__ int s_seq;
     __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
-    __shared__ int s_abort;
     float *s_o = reinterpret_cast<float *>(smem + C::kRing);
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const int cta = blockIdx.x;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < C::kStages; i++)
-            mbar_init(&s_bar[warp][i], 1);
-        fence_barrier_init();
-    }
-    if (tid == 0)
-        s_abort = 0;
     griddep_wait();
 
     // ---- this CTA's share of the list
     const Kv4Seqs &sq = p.a.s;
     int row0, n, len, nt, nrb;
-    int64_t first = tid < sq.nseq ? sequence<D, NT>(p, tid, row0, n, len, nt, nrb) : 0;
+    int64_t first = tid < sq.nseq ? sequence<D, NT, FOLD>(p, tid, row0, n, len, nt, nrb) : 0;
     int64_t total = 0, sum = 0;
     for (int base = 0; base < sq.nseq; base += kThreads) {
         int64_t v = first, all;
         if (base)
-            v = base + tid < sq.nseq ? sequence<D, NT>(p, base + tid, row0, n, len, nt, nrb) : 0;
+            v = base + tid < sq.nseq ? sequence<D, NT, FOLD>(p, base + tid, row0, n, len, nt, nrb) : 0;
         block_sum_scan(v, s_scan, all);
         total += all;
     }
@@ -241,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
     for (int base = 0; base < sq.nseq; base += kThreads) {
         int64_t v = first, all;
         if (base)
-            v = base + tid < sq.nseq ? sequence<D, NT>(p, base + tid, row0, n, len, nt, nrb) : 0;
+            v = base + tid < sq.nseq ? sequence<D, NT, FOLD>(p, base + tid, row0, n, len, nt, nrb) : 0;
         const int64_t end = sum + block_sum_scan(v, s_scan, all);
         if (end - v <= x0 && x0 < end) {
             s_seq = base + tid;
@@ -252,52 +264,92 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
     __syncthreads();
     griddep_launch_dependents();
 
-    Walk<D, NT> seg, ahead;
+    Walk<D, NT, FOLD> seg, ahead;
     seg.start(p, x0, x1, s_seq, x0 - s_from);
     ahead = seg;
 
-    // ---- the warp's ring of tiles
+    // ---- the warp's ring of tiles, filled by 16-byte asynchronous copies of all its lanes (a
+    // bulk copy per page takes its operands from the warp, not the lane: 15% slower here)
     uint8_t *ring = smem + warp * (C::kStages * C::kStageBytes);
+    const uint32_t ring_at = smem_u32(ring) + lane * 16;
     const int ps = sq.page_size();
-    const int64_t page_bytes = kv4_page_bytes(ps, D);
-    const int slice = min(ps, C::kTile);               // keys per page of a tile
-    int next_tile = ahead.t0 + warp, issued = 0, used = 0;
+    const int64_t page_bytes = kv4_page_bytes(ps, D), page_stride = sq.Hkv * page_bytes;
+    const int slice = min(ps, C::kTile);               // keys of a tile that one page holds
+    // this lane's 16 bytes of a page's first rows (256 / D of a row's codes), and of its
+    // params (lanes 0-15 the keys', 16-31 the values')
+    constexpr int kRowStep = 1024 / D;                 // rows of codes that 512 bytes hold
+    const int code_row = lane / (D / 32), par_row = lane % 16 * (4 / kG);
+    const int64_t par_off = (int64_t)ps * D + (lane / 16) * (ps * kG * 4) + lane % 16 * 16;
+    const uint8_t *head;                               // the segment's head in page 0
+    int next_tile, ids = 0, stage_in = 0;
     bool more = true;
-    auto issue = [&]() {
-        while (more && next_tile >= ahead.t1) {
-            more = ahead.next(p);
-            next_tile = ahead.t0 + warp;
+    // steps to the warp's next tile and looks up its pages (lane i: the i-th), one tile ahead
+    // of their use
+    auto advance = [&]() {
+        if (next_tile >= ahead.t1) {
+            do {
+                more = more && ahead.next(p);
+                next_tile = ahead.t0 + warp;
+            } while (more && next_tile >= ahead.t1);
+            head = sq.cache + ahead.kvh * page_bytes;
         }
-        if (!more)
-            return;
-        const int k0 = next_tile * C::kTile;
-        const int rows = min(C::kTile, (ahead.len + 15) / 16 * 16 - k0);   // rows to fetch
-        const int cnt = min(slice, rows - lane * slice);                   // this lane's
-        int page = -1;
-        if (cnt > 0)
-            page = sq.page(ahead.s, k0 + lane * slice);
-        uint64_t *bar = &s_bar[warp][issued % C::kStages];
-        uint8_t *dst = ring + issued % C::kStages * C::kStageBytes;
-        const int bytes = page >= 0 ? cnt * (D + 8 * kG) : 0;
-        const int all = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0)
-            mbar_arrive_expect_tx(bar, all);
-        __syncwarp();
-        if (page >= 0) {
-            const int row = (k0 + lane * slice) & (ps - 1), at = lane * slice;
-            const uint8_t *src = sq.cache + ((int64_t)page * sq.Hkv + ahead.kvh) * page_bytes;
-            bulk_load_g2s(dst + at * (D / 2), src + row * (D / 2), cnt * (D / 2), bar);
-            bulk_load_g2s(dst + (C::kTile + at) * (D / 2), src + (ps + row) * (D / 2), cnt * (D / 2), bar);
-            bulk_load_g2s(dst + C::kTile * D + at * kG * 4, src + ps * D + row * kG * 4, cnt * kG * 4, bar);
-            bulk_load_g2s(dst + C::kTile * D + C::kParBytes + at * kG * 4,
-                          src + ps * D + (ps + row) * kG * 4, cnt * kG * 4, bar);
-        }
-        next_tile += kWarps;
-        issued++;
+        const int key = next_tile * C::kTile + lane * slice;
+        ids = 0;
+        if (more && lane * slice < C::kTile && key < ahead.len)
+            ids = __ldg(sq.block_table + (int64_t)ahead.s * sq.max_pages + (key >> sq.page_log2));
     };
+    auto issue = [&]() {
+        if (more) {
+            const int k0 = next_tile * C::kTile, left = ahead.len - k0;
+            const uint32_t dst = ring_at + stage_in;
+            // a table entry that is no page: its status bit is set and page 0 read in its place
+            if ((uint32_t)ids >= (uint32_t)sq.num_pages) {
+                atomicOr(sq.status, status_bit(SAGE_ERR_BAD_PAGE));
+                ids = 0;
+            }
+            __syncwarp();
+            if (slice == C::kTile && left >= C::kTile) {   // a whole tile of one page
+                const int row = k0 & (ps - 1);
+                const uint8_t *src = head + __shfl_sync(0xffffffffu, ids, 0) * page_stride;
+                const uint8_t *kc = src + row * (D / 2) + lane * 16, *vc = kc + ps * (D / 2);
 #pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    copy16(dst + i * 512, kc + i * 512);
+                    copy16(dst + C::kTile * (D / 2) + i * 512, vc + i * 512);
+                }
+                copy16(dst + C::kTile * D, src + par_off + row * (kG * 4));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int at = i * kRowStep + code_row;    // at / slice is the same for all lanes
+                    const int id = __shfl_sync(0xffffffffu, ids, i * kRowStep / slice);
+                    const int row = (k0 + at) & (ps - 1);
+                    const uint8_t *kc = head + id * page_stride + row * (D / 2) + lane % (D / 32) * 16;
+                    if (at < left) {
+                        copy16(dst + i * 512, kc);
+                        copy16(dst + C::kTile * (D / 2) + i * 512, kc + ps * (D / 2));
+                    }
+                }
+                const int id = __shfl_sync(0xffffffffu, ids, par_row / slice);
+                const int row = (k0 + par_row) & (ps - 1);
+                if (par_row < left)
+                    copy16(dst + C::kTile * D, head + id * page_stride + par_off +
+                                                   (row - par_row) * (kG * 4));
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        stage_in = stage_in + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : stage_in + C::kStageBytes;
+        next_tile += kWarps;
+        if (more)
+            advance();
+    };
+    next_tile = ahead.t0 + warp;
+    head = sq.cache + ahead.kvh * page_bytes;
+    advance();
+#pragma unroll 1
     for (int i = 0; i < C::kStages; i++)
         issue();
+    int stage_out = 0;
 
     int tail_last = -1;
     Tail tail_info = {-1, 0, 0, 0, 0};
@@ -310,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
         int lim[NT][2];
 #pragma unroll
         for (int nt8 = 0; nt8 < NT; nt8++) {
-            const int r = nt8 * 8 + g;
-            float x[kG][16];
+            const int r = FOLD ? g % 4 : nt8 * 8 + g;
+            float x[kG][16], sum[kG];
             float big = 0.0f;
             const int qi = (r0 + r) / p.group, hh = (r0 + r) % p.group;
             const int64_t off = (int64_t)(seg.row0 + qi) * p.a.q_tok +
@@ -341,20 +393,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                s *= p.sc_log2;
-                qs[nt8][gr][0] = __shfl_sync(0xffffffffu, s, t4 * 8);
-                qs[nt8][gr][1] = __shfl_sync(0xffffffffu, s, t4 * 8 + 4);
+                sum[gr] = s;
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             // the row as fp16 with its largest element in [2^14, 2^15): a factor 2^(14 - e)
             const int e = max(-100, min(100, (int)(__float_as_uint(big) >> 23) - 127));
             const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            const float back = __uint_as_float((uint32_t)(127 + 10 + e) << 23) * p.sc_log2;   // 2^(24 - 14 + e)
+            const float unit = __uint_as_float((uint32_t)(127 + 10 + e) << 23);   // 2^(24 - 14 + e)
+            const float back = unit * p.sc_log2;
             f[nt8][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
             f[nt8][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
 #pragma unroll
-            for (int gr = 0; gr < kG; gr++)
+            for (int gr = 0; gr < kG; gr++) {
+                sum[gr] *= 1.0f / unit;                // exact: a power of two
+                qs[nt8][gr][0] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8);
+                qs[nt8][gr][1] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8 + 4);
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
                     const float *w = x[gr] + 8 * j;
@@ -364,21 +418,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                     qf[nt8][gr][j][2] = pack_half2(w[2] * scale, w[6] * scale);
                     qf[nt8][gr][j][3] = pack_half2(w[3] * s16, w[7] * s16);
                 }
+            }
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                const int rr = nt8 * 8 + 2 * t4 + c;
+                const int rr = FOLD ? (2 * t4 + c) % 4 : nt8 * 8 + 2 * t4 + c;
                 lim[nt8][c] = p.a.causal && rr < nrows ? seg.len - seg.n + (r0 + rr) / p.group : seg.len - 1;
             }
         }
         // keys up to here are seen by every row of the block
         const int seen = p.a.causal ? min(seg.len - 1, seg.len - seg.n + r0 / p.group) : seg.len - 1;
 
-        float m[NT][2], l[NT][2], o2[NT][kG][2], o[NT][kG][4][4];
+        float nm[NT][2], l[NT][2], o2[NT][kG][2], o[NT][kG][4][4];   // nm: -m
 #pragma unroll
         for (int i = 0; i < NT; i++) {
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                m[i][c] = -INFINITY;
+                nm[i][c] = INFINITY;
                 l[i][c] = 0.0f;
             }
 #pragma unroll
@@ -391,34 +446,30 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                         o[i][gr][j][c] = 0.0f;
             }
         }
+        const float2 low_sel = t4 < 2 ? make_float2(0.0f, 0.0f) : make_float2(-1.0f, -1.0f);
         int vexp = -64;                                // exponent the value products are scaled for
 
         for (int t = seg.t0 + warp; t < seg.t1; t += kWarps) {
             const int k0 = t * C::kTile;
-            const uint8_t *st = ring + used % C::kStages * C::kStageBytes;
-            mbar_wait(&s_bar[warp][used % C::kStages], (used / C::kStages) & 1, &s_abort, sq.status,
-                      status_bit(SAGE_ERR_TIMEOUT), kTimeoutNs);
+            const uint8_t *st = ring + stage_out;
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+            __syncwarp();                              // every lane's part has landed
             const bool masked = k0 + C::kTile - 1 > seen;
 
-            // ---- scores, S^T: rows are keys, columns query rows
+            // ---- scores, S^T: rows are keys, columns query rows; s f is the base-2 logit
             float s[kKB][NT][4];
-            const __half2 *kpar = reinterpret_cast<const __half2 *>(st + C::kTile * D);
+            const uint32_t *kpar = reinterpret_cast<const uint32_t *>(st + C::kTile * D);
 #pragma unroll
             for (int kb = 0; kb < kKB; kb++) {
                 const uint8_t *r0p = st + (kb * 16 + g) * (D / 2) + t4 * 8;
                 const uint8_t *r1p = r0p + 8 * (D / 2);
-                float add[NT][4];
-#pragma unroll
-                for (int i = 0; i < NT; i++)
-#pragma unroll
-                    for (int c = 0; c < 4; c++)
-                        s[kb][i][c] = add[i][c] = 0.0f;
+                float2 p0[kG], p1[kG];
+                load_params<kG>(kpar + (kb * 16 + g) * kG, p0);
+                load_params<kG>(kpar + (kb * 16 + g + 8) * kG, p1);
 #pragma unroll
                 for (int gr = 0; gr < kG; gr++) {
                     const uint2 w0 = *reinterpret_cast<const uint2 *>(r0p + gr * 32);
                     const uint2 w1 = *reinterpret_cast<const uint2 *>(r1p + gr * 32);
-                    const float2 p0 = __half22float2(kpar[(kb * 16 + g) * kG + gr]);
-                    const float2 p1 = __half22float2(kpar[(kb * 16 + g + 8) * kG + gr]);
                     float acc[NT][4] = {};
 #pragma unroll
                     for (int j = 0; j < 2; j++) {
@@ -434,22 +485,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < NT; i++) {
-                        s[kb][i][0] = fmaf(p0.x, acc[i][0], s[kb][i][0]);
-                        s[kb][i][1] = fmaf(p0.x, acc[i][1], s[kb][i][1]);
-                        s[kb][i][2] = fmaf(p1.x, acc[i][2], s[kb][i][2]);
-                        s[kb][i][3] = fmaf(p1.x, acc[i][3], s[kb][i][3]);
-                        add[i][0] = fmaf(p0.y, qs[i][gr][0], add[i][0]);
-                        add[i][1] = fmaf(p0.y, qs[i][gr][1], add[i][1]);
-                        add[i][2] = fmaf(p1.y, qs[i][gr][0], add[i][2]);
-                        add[i][3] = fmaf(p1.y, qs[i][gr][1], add[i][3]);
-                    }
+                    for (int i = 0; i < NT; i++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            const float2 pr = c < 2 ? p0[gr] : p1[gr];
+                            const float low = gr == 0 ? pr.y * qs[i][gr][c & 1] : fmaf(pr.y, qs[i][gr][c & 1], s[kb][i][c]);
+                            s[kb][i][c] = fmaf(pr.x, acc[i][c], low);
+                        }
                 }
-#pragma unroll
-                for (int i = 0; i < NT; i++)
-#pragma unroll
-                    for (int c = 0; c < 4; c++)
-                        s[kb][i][c] = fmaf(s[kb][i][c], f[i][c & 1], add[i][c]);
             }
             uint32_t hidden = 0;                       // of this lane's scores, bit kb*NT*4 + ...
             if (masked) {
@@ -465,38 +508,36 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                             }
             }
 
-            // ---- running maximum and the factor of what was summed before
-            float alpha[NT][2], base[NT][2];
+            // ---- the reference m that probabilities are taken relative to moves only when a
+            // logit is more than 8 above it, so p <= 2^8
+            float alpha[NT][2];
+            float x[NT][2];
             bool move = false;
 #pragma unroll
             for (int i = 0; i < NT; i++)
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    float x = -INFINITY;
+                    x[i][c] = fmaxf(s[0][i][c], s[0][i][c + 2]);
 #pragma unroll
-                    for (int kb = 0; kb < kKB; kb++)
-                        x = fmaxf(x, fmaxf(s[kb][i][c], s[kb][i][c + 2]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    x = fmaxf(x, m[i][c]);
-                    base[i][c] = x == -INFINITY ? 0.0f : x;
-                    alpha[i][c] = ex2_approx(m[i][c] - base[i][c]);
-                    move |= x != m[i][c];
-                    m[i][c] = x;
+                    for (int kb = 1; kb < kKB; kb++)
+                        x[i][c] = fmaxf(x[i][c], fmaxf(s[kb][i][c], s[kb][i][c + 2]));
+                    alpha[i][c] = 1.0f;
+                    move |= fmaf(x[i][c], f[i][c], nm[i][c]) > 8.0f;
                 }
-            // ---- the tile's largest value step: the products p * step are scaled by a power of
-            // two that keeps them below 2^15 and the largest near 2^11, whatever V's size
-            const __half2 *vpar = reinterpret_cast<const __half2 *>(st + C::kTile * D + C::kParBytes);
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < C::kTile * kG / 32; i++) {
-                const int e = lane + 32 * i;
-                const uint32_t b = reinterpret_cast<const uint32_t *>(vpar)[e] & 0xFFFFu;
-                if (k0 + e / kG < seg.len && b < 0x7C00u)
-                    top = max(top, b);
+            // ---- the tile's largest value step: products p * step are scaled by a power of two
+            // that keeps them below 2^15, whatever V's size. In a masked tile, rows behind the last
+            // token and non-finite steps do not count (elsewhere every row sees every step)
+            const uint32_t *vpar = reinterpret_cast<const uint32_t *>(st + C::kTile * D + C::kParBytes);
+            uint2 vs = reinterpret_cast<const uint2 *>(vpar)[lane];
+            vs.x &= 0x7FFFu;
+            vs.y &= 0x7FFFu;
+            if (masked) {
+                if (vs.x >= 0x7C00u || k0 + 2 * lane / kG >= seg.len)
+                    vs.x = 0;
+                if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= seg.len)
+                    vs.y = 0;
             }
-            const int texp = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+            const int texp = (int)(__reduce_max_sync(0xffffffffu, max(vs.x, vs.y)) >> 10);
             float shift = 1.0f;
             if (texp > vexp + 3) {
                 shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
@@ -508,6 +549,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                 for (int i = 0; i < NT; i++)
 #pragma unroll
                     for (int c = 0; c < 2; c++) {
+                        float y = x[i][c];
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) * f[i][c];
+                        if (y > -nm[i][c]) {           // (rows that have seen no key: -inf on both sides)
+                            alpha[i][c] = ex2_approx(-nm[i][c] - y);
+                            nm[i][c] = -y;
+                        }
                         l[i][c] *= alpha[i][c];
                         const float as = alpha[i][c] * shift;
 #pragma unroll
@@ -521,48 +570,65 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                         }
                     }
             }
-            const float vscale = __uint_as_float((uint32_t)(127 + 26 - vexp) << 23);
+            const float vscale = __uint_as_float((uint32_t)(127 + 18 - vexp) << 23);
 
             // ---- probabilities and O^T += V^T P^T: rows are channels, columns query rows
 #pragma unroll
             for (int kb = 0; kb < kKB; kb++) {
 #pragma unroll
-                for (int i = 0; i < NT; i++)
-#pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        s[kb][i][c] = ex2_approx(s[kb][i][c] - base[i][c & 1]);
-                        l[i][c & 1] += s[kb][i][c];
-                    }
+                for (int i = 0; i < NT; i++) {
+                    const float2 ff = make_float2(f[i][0], f[i][1]);
+                    // a row that has seen no key yet: 2^(-inf + 0)
+                    const float2 nn = make_float2(nm[i][0] == INFINITY ? 0.0f : nm[i][0],
+                                                  nm[i][1] == INFINITY ? 0.0f : nm[i][1]);
+                    const float2 ta = fma2(make_float2(s[kb][i][0], s[kb][i][1]), ff, nn);
+                    const float2 tb = fma2(make_float2(s[kb][i][2], s[kb][i][3]), ff, nn);
+                    s[kb][i][0] = ex2_approx(ta.x);
+                    s[kb][i][1] = ex2_approx(ta.y);
+                    s[kb][i][2] = ex2_approx(tb.x);
+                    s[kb][i][3] = ex2_approx(tb.y);
+                    const float2 ls = add2(make_float2(s[kb][i][0], s[kb][i][1]), make_float2(s[kb][i][2], s[kb][i][3]));
+                    const float2 lt = add2(make_float2(l[i][0], l[i][1]), ls);
+                    l[i][0] = lt.x;
+                    l[i][1] = lt.y;
+                }
                 const uint8_t *vr = st + (C::kTile + kb * 16 + 2 * t4) * (D / 2) + g * 4;
+                float2 p0[kG], p1[kG];
+                load_params<kG>(vpar + (kb * 16 + g) * kG, p0);
+                load_params<kG>(vpar + (kb * 16 + g + 8) * kG, p1);
 #pragma unroll
                 for (int gr = 0; gr < kG; gr++) {
-                    const float2 p0 = __half22float2(vpar[(kb * 16 + g) * kG + gr]);
-                    const float2 p1 = __half22float2(vpar[(kb * 16 + g + 8) * kG + gr]);
-                    const float step0 = p0.x * vscale, step1 = p1.x * vscale;
-                    const float mid0 = fmaf(8.0f, p0.x, p0.y), mid1 = fmaf(8.0f, p1.x, p1.y);
+                    const float step0 = p0[gr].x * vscale, step1 = p1[gr].x * vscale;
+                    const float mid0 = fmaf(8.0f, p0[gr].x, p0[gr].y), mid1 = fmaf(8.0f, p1[gr].x, p1[gr].y);
                     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
                     for (int i = 0; i < NT; i++) {
-                        float pv[4], pm[4];
+                        float pv[4];
 #pragma unroll
-                        for (int c = 0; c < 4; c++) {
+                        for (int c = 0; c < 4; c++)
                             pv[c] = s[kb][i][c] * (c < 2 ? step0 : step1);
-                            pm[c] = s[kb][i][c] * (c < 2 ? mid0 : mid1);
-                        }
                         if (masked) {                  // 0 times what lies in a hidden place is 0
 #pragma unroll
+                            for (int c = 0; c < 4; c++) {
+                                const bool hid = hidden >> ((kb * NT + i) * 4 + c) & 1;
+                                pv[c] = hid ? 0.0f : pv[c];
+                                o2[i][gr][c & 1] = hid ? o2[i][gr][c & 1]
+                                                       : fmaf(s[kb][i][c], c < 2 ? mid0 : mid1, o2[i][gr][c & 1]);
+                            }
+                        } else {
+#pragma unroll
                             for (int c = 0; c < 4; c++)
-                                if (hidden >> ((kb * NT + i) * 4 + c) & 1)
-                                    pv[c] = pm[c] = 0.0f;
+                                o2[i][gr][c & 1] = fmaf(s[kb][i][c], c < 2 ? mid0 : mid1, o2[i][gr][c & 1]);
                         }
-                        o2[i][gr][0] += pm[0] + pm[2];
-                        o2[i][gr][1] += pm[1] + pm[3];
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const __half2 a = __floats2half2_rn(pv[2 * h], pv[2 * h + 1]);
-                            const float2 b = __half22float2(a);
-                            hi[i][h] = transpose8x8(h2_bits(a));
-                            lo[i][h] = transpose8x8(pack_half2(pv[2 * h] - b.x, pv[2 * h + 1] - b.y));
+                            const float2 v = make_float2(pv[2 * h], pv[2 * h + 1]);
+                            const __half2 a = __floats2half2_rn(v.x, v.y);
+                            // FOLD: this lane's columns take the high term (0) or the low one (-1)
+                            const float2 d = fma2(__half22float2(a), FOLD ? low_sel : make_float2(-1.0f, -1.0f), v);
+                            hi[i][h] = transpose8x8(FOLD ? pack_half2(d.x, d.y) : h2_bits(a));
+                            if (!FOLD)
+                                lo[i][h] = transpose8x8(pack_half2(d.x, d.y));
                         }
                     }
                     // keys 2t, 2t+1 (A, B) and 2t+8, 2t+9 (C, D) of the block; 8 channels each
@@ -586,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
 #pragma unroll
                             for (int i = 0; i < NT; i++) {
                                 mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, hi[i][0], hi[i][1]);
-                                mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, lo[i][0], lo[i][1]);
+                                if (!FOLD)
+                                    mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, lo[i][0], lo[i][1]);
                             }
                             ab >>= 8;
                             cd >>= 8;
@@ -595,18 +662,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                 }
             }
             __syncwarp();                              // the stage is read
-            used++;
+            stage_out = stage_out + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : stage_out + C::kStageBytes;
             issue();
         }
 
         // ---- merge the warps: maximum, weight and sums of each row through shared memory
-        const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 - 26 + vexp) << 23);
+        const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 - 18 + vexp) << 23);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                const int r = i * 8 + 2 * t4 + c;
+                const int r = FOLD ? (2 * t4 + c) % 4 : i * 8 + 2 * t4 + c;
                 float lw = l[i][c], ow[kG];
+                if (FOLD) {                            // high and low terms' columns
+#pragma unroll
+                    for (int gr = 0; gr < kG; gr++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            o[i][gr][j][c] += __shfl_xor_sync(0xffffffffu, o[i][gr][j][c], 2);
+                            o[i][gr][j][c + 2] += __shfl_xor_sync(0xffffffffu, o[i][gr][j][c + 2], 2);
+                        }
+                }
 #pragma unroll
                 for (int gr = 0; gr < kG; gr++)
                     ow[gr] = o2[i][gr][c];
@@ -618,10 +694,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
                         ow[gr] += __shfl_xor_sync(0xffffffffu, ow[gr], x);
                 }
                 if (g == 0) {
-                    s_m[warp][r] = m[i][c];
+                    s_m[warp][r] = -nm[i][c];
                     s_l[warp][r] = lw;
                 }
-                if (r < nrows) {
+                if (r < nrows && !(FOLD && t4 >= 2)) {
                     float *dst = s_o + (warp * C::kRows + r) * C::kPitch + g * 8;
 #pragma unroll
                     for (int gr = 0; gr < kG; gr++)
@@ -690,11 +766,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
         any = seg.next(p);
         __syncthreads();                               // the merge buffer is free again
     }
-    // a wait that gave up: let this warp's own copies land before the CTA's memory is reused
-    if (s_abort)
-        for (; used < issued; used++)
-            mbar_wait(&s_bar[warp][used % C::kStages], (used / C::kStages) & 1, nullptr, sq.status,
-                      status_bit(SAGE_ERR_TIMEOUT), kTimeoutNs);
     if (tid == 0) {
         tail_info.last = tail_last;
         p.tail[cta] = tail_info;
@@ -702,10 +773,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kCtasPerSM)) kv4_attn_k
 }
 
 // Merge of what several CTAs share: CTA (c, r) takes row r of the segment that CTA c began.
-template <int D, int NT>
+template <int D, int NT, bool FOLD>
 __global__ void __launch_bounds__(D) kv4_attn_merge(const Params p)
 {
-    using C = Cfg<D, NT>;
+    using C = Cfg<D, NT, FOLD>;
     griddep_wait();
     const int c0 = blockIdx.x, r = blockIdx.y, ch = threadIdx.x;
     const Tail t = p.tail[c0];
@@ -738,19 +809,25 @@ __global__ void __launch_bounds__(D) kv4_attn_merge(const Params p)
         p.a.lse[row * p.a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// Rows of a pass: 8 where the queries of a key head fit, else 16.
-int query_tiles(int Hq, int Hkv, int max_q) { return max_q * (Hq / Hkv) <= 8 ? 1 : 2; }
-int ctas(int nt) { return nt == 1 ? 2 * kSMs : kSMs; }
+// What takes a call's rows per key head: the folded tile up to 4, one tile up to 8, else two.
+int variant(int Hq, int Hkv, int max_q)
+{
+    const int rows = max_q * (Hq / Hkv);
+    return rows <= 4 ? 0 : rows <= 8 ? 1 : 2;
+}
+int ctas(int var) { return var < 2 ? 2 * kSMs : kSMs; }
+int rows_of(int var) { return 4 << var; }
 
-template <int D, int NT>
+template <int D, int NT, bool FOLD>
 cudaError_t launch(const Params &p, cudaStream_t st)
 {
-    using C = Cfg<D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>,
+    using C = Cfg<D, NT, FOLD>;
+    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT, FOLD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess)
         return e;
-    kv4_attn_kernel<D, NT><<<ctas(NT), kThreads, C::kSmem, st>>>(p);
+    const int n = C::kCtasPerSM * kSMs;
+    kv4_attn_kernel<D, NT, FOLD><<<n, kThreads, C::kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     const int rows = std::min(C::kRows, p.a.max_q * p.group);
@@ -758,36 +835,38 @@ cudaError_t launch(const Params &p, cudaStream_t st)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas(NT), rows);
+    cfg.gridDim = dim3(n, rows);
     cfg.blockDim = dim3(D);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_attn_merge<D, NT>, p);
+    return cudaLaunchKernelEx(&cfg, kv4_attn_merge<D, NT, FOLD>, p);
 }
 
-size_t tail_bytes(int nt) { return (sizeof(Tail) * ctas(nt) + 255) / 256 * 256; }
+size_t tail_bytes(int var) { return (sizeof(Tail) * ctas(var) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t kv4_attn_workspace(int Hq, int Hkv, int max_q, int d)
 {
-    const int nt = query_tiles(Hq, Hkv, max_q);
-    return tail_bytes(nt) + (size_t)ctas(nt) * 2 * 8 * nt * (d + 2) * sizeof(float);
+    const int var = variant(Hq, Hkv, max_q);
+    return tail_bytes(var) + (size_t)ctas(var) * 2 * rows_of(var) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t st)
 {
-    const int nt = query_tiles(a.Hq, a.s.Hkv, a.max_q);
+    const int var = variant(a.Hq, a.s.Hkv, a.max_q);
     Params p;
     p.a = a;
     p.tail = static_cast<Tail *>(a.workspace);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + tail_bytes(nt));
+    p.part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + tail_bytes(var));
     p.group = a.Hq / a.s.Hkv;
     p.sc_log2 = a.sm_scale * kLog2e;
     if (a.d == 128)
-        return nt == 1 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
-    return nt == 1 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
+        return var == 0   ? launch<128, 1, true>(p, st)
+               : var == 1 ? launch<128, 1, false>(p, st)
+                          : launch<128, 2, false>(p, st);
+    return var == 0 ? launch<64, 1, true>(p, st) : var == 1 ? launch<64, 1, false>(p, st) : launch<64, 2, false>(p, st);
 }
 
 }  // namespace sage

@@ -144,7 +144,7 @@ def _attn(lib, q=FAKE, cache=FAKE, table=FAKE, lens=FAKE, cu=FAKE, out=FAKE, lse
 
 def test_attn_refusals(lib):
     bad, uns, mis = sage.SAGE_ERR_INVALID_ARG, sage.SAGE_ERR_UNSUPPORTED, sage.SAGE_ERR_MISALIGNED
-    for name in ("q", "cache", "table", "lens", "out", "ws", "max_q"):
+    for name in ("q", "cache", "table", "lens", "out", "ws", "max_q", "pages"):
         assert _attn(lib, **{name: 0}) == bad, name
     assert _attn(lib, Hq=5) == bad and _attn(lib, Hkv=0) == bad and _attn(lib, max_q=-1) == bad
     assert _attn(lib, max_q=17) == uns and _attn(lib, page=12) == uns and _attn(lib, d=32) == uns
