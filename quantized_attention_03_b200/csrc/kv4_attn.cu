@@ -44,6 +44,17 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSMs = 148;
+// Places that the start of a segment takes in the list of work, in tiles: what it costs a CTA
+// to start on one (queries, pages, first tile, merge), or a warp that works alone.
+#ifndef SOLOC
+#define SOLOC 2
+#endif
+#ifndef SOLOS
+#define SOLOS 148
+#endif
+constexpr int kTeamCost = 16, kSoloCost = SOLOC;
+// From so many segments on, every warp works alone on its own share; below, a CTA's warps share one.
+constexpr int kSoloSegments = SOLOS;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -59,7 +70,7 @@ struct Cfg {
     static constexpr int kRows = FOLD ? 4 : 8 * NT;
     static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
     static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
-    static constexpr int kPitch = D + 4;               // floats between rows of the merge buffer
+    static constexpr int kPitch = D + 4;               // floats of a partial row: sums, reference, weight
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kSmem = kRing + kWarps * kRows * kPitch * 4;
 };
@@ -72,8 +83,9 @@ struct Tail {
 
 struct Params {
     Kv4AttnArgs a;
-    float *part;          // [ctas][2][rows][D + 2]: sums, then maximum and weight
-    Tail *tail;           // [ctas]
+    int *solo;            // whether warps work alone, for the merge
+    float *part;          // [teams][2][rows][D + 4]: sums, then reference and weight
+    Tail *tail;           // [teams]
     int group;            // query heads per key head
     float sc_log2;
 };
@@ -125,10 +137,76 @@ __device__ __forceinline__ void load_params(const uint32_t *at, float2 (&p)[G])
     }
 }
 
-// Tiles of a sequence: row blocks x key heads x key tiles; at least one tile where it has
-// queries, so that queries without keys are written too.
+// N channels from `ch` on of an output row, acc / L, and with the first of them its lse.
+template <int N>
+__device__ __forceinline__ void write_row(const Kv4AttnArgs &a, int64_t row, int head, int d, int ch, float M, float L,
+                                          const float *acc)
+{
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int64_t at = (row * a.Hq + head) * d + ch;
+    uint32_t u[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; i++)
+        if (a.bf16)
+            *reinterpret_cast<__nv_bfloat162 *>(u + i) = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+        else
+            u[i] = pack_half2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    uint16_t *out = static_cast<uint16_t *>(a.out) + at;
+    if constexpr (N == 4)
+        *reinterpret_cast<uint2 *>(out) = make_uint2(u[0], u[1]);
+    else
+        *reinterpret_cast<uint32_t *>(out) = u[0];
+    if (ch == 0 && a.lse)
+        a.lse[row * a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// A query row's operands for the key product: this lane holds 16 channels of each group, u[g]
+// the 16-bit input. Operand 0 of an 8-channel word is channels (0, 4), 1 is (1, 5) / 16, 2 is
+// (2, 6), 3 is (3, 7) / 16, as the masked codes have them. The row is scaled by a power of two
+// so that its largest element is in [2^14, 2^15); returned is what a product's units are worth,
+// 2^24 over that factor (the codes are 2^-24).
+template <int G>
+__device__ __forceinline__ float query_row(const uint4 (&u)[G][2], int bf16, uint32_t (&qf)[G][2][4])
+{
+    float big;
+    if (bf16) {
+        __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+#pragma unroll
+        for (int i = 0; i < G * 8; i++)
+            m = __hmax2(m, __habs2(reinterpret_cast<const __nv_bfloat162 *>(&u[i / 8][i / 4 % 2])[i % 4]));
+        big = fmaxf(__low2float(m), __high2float(m));
+    } else {
+        __half2 m = __float2half2_rn(0.0f);
+#pragma unroll
+        for (int i = 0; i < G * 8; i++)
+            m = __hmax2(m, __habs2(reinterpret_cast<const __half2 *>(&u[i / 8][i / 4 % 2])[i % 4]));
+        big = fmaxf(__low2float(m), __high2float(m));
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const int e = max(-100, min(100, (int)(__float_as_uint(big) >> 23) - 127));
+    const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23), s16 = scale * 0.0625f;
+#pragma unroll
+    for (int gr = 0; gr < G; gr++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            float w[8];
+            if (bf16)
+                load8<__nv_bfloat16>(u[gr][j], w);
+            else
+                load8<__half>(u[gr][j], w);
+            qf[gr][j][0] = pack_half2(w[0] * scale, w[4] * scale);
+            qf[gr][j][1] = pack_half2(w[1] * s16, w[5] * s16);
+            qf[gr][j][2] = pack_half2(w[2] * scale, w[6] * scale);
+            qf[gr][j][3] = pack_half2(w[3] * s16, w[7] * s16);
+        }
+    return __uint_as_float((uint32_t)(127 + 10 + e) << 23);   // 2^(24 - 14 + e)
+}
+
+// Segments of a sequence (key heads x row blocks) and tiles of each; at least one tile where it
+// has queries, so that queries without keys are written too.
 template <int D, int NT, bool FOLD>
-__device__ __forceinline__ int64_t sequence(const Params &p, int s, int &row0, int &n, int &len, int &nt, int &nrb)
+__device__ __forceinline__ int sequence(const Params &p, int s, int &row0, int &n, int &len, int &nt, int &nrb)
 {
     using C = Cfg<D, NT, FOLD>;
     int a, b;
@@ -145,47 +223,53 @@ __device__ __forceinline__ int64_t sequence(const Params &p, int s, int &row0, i
     }
     nt = max(1, (len + C::kTile - 1) / C::kTile);
     nrb = (n * p.group + C::kRows - 1) / C::kRows;
-    return (int64_t)nt * nrb * p.a.s.Hkv;
+    return nrb * p.a.s.Hkv;
 }
 
-// A walk over the segments (sequence, key head, row block, range of tiles) of a CTA's share
-// [x, x1) of the list.
+// A walk over the segments (sequence, key head, row block, range of tiles) of a share [from, to)
+// of the list, in which a segment is `cost` places of start-up and its tiles.
 template <int D, int NT, bool FOLD>
 struct Walk {
-    int64_t x, x1;
-    int s, row0, n, len, nt, nrb;     // the sequence
-    int kvh, rb, t0, t1;              // the segment
+    int64_t x, to;                    // where the segment begins in the list, and the share ends
+    int cost, s, row0, n, len, nt, nrb;   // the sequence
+    int kvh, rb, t0, t1;              // the segment; t0 == t1: nothing of it is in the share
+    bool live;                        // there is a segment
 
-    __device__ void start(const Params &p, int64_t from, int64_t to, int seq, int64_t offset)
+    __device__ void start(const Params &p, int start_cost, int64_t from, int64_t end, int seq, int64_t offset)
     {
-        x = from;
-        x1 = to;
+        cost = start_cost;
+        to = end;
         s = seq;
         sequence<D, NT, FOLD>(p, s, row0, n, len, nt, nrb);
-        const int h = (int)(offset / nt);
-        t0 = (int)(offset % nt);
+        const int each = nt + cost, h = (int)(offset / each), at = (int)(offset % each);
+        x = from - at;
         kvh = h / nrb;
         rb = h % nrb;
-        t1 = (int)min((int64_t)nt, t0 + (x1 - x));
+        t0 = max(0, at - cost);
+        t1 = (int)min((int64_t)nt, max((int64_t)t0, to - x - cost));
+        live = true;
+        if (t0 >= t1)
+            next(p);
     }
-    __device__ bool next(const Params &p)
+    __device__ void next(const Params &p)
     {
-        x += t1 - t0;
-        if (x >= x1)
-            return false;
-        t0 = 0;
+        x += nt + cost;
+        live = false;
+        if (x + cost >= to)
+            return;
         if (++rb == nrb) {
             rb = 0;
             if (++kvh == p.a.s.Hkv) {
                 kvh = 0;
                 do {
                     if (++s >= p.a.s.nseq)
-                        return false;
+                        return;
                 } while (sequence<D, NT, FOLD>(p, s, row0, n, len, nt, nrb) == 0);
             }
         }
-        t1 = (int)min((int64_t)nt, x1 - x);
-        return true;
+        t0 = 0;
+        t1 = (int)min((int64_t)nt, to - x - cost);
+        live = true;
     }
 };
 
@@ -221,52 +305,88 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
     constexpr int kG = C::kGroups, kKB = C::kTile / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[kWarps];
-    __shared__ int64_t s_from;
-    __shared__ int s_seq;
-    __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
+    __shared__ int64_t s_x[kWarps + 1], s_from[kWarps];
+    __shared__ int s_seq[kWarps], s_segments;
+    __shared__ Walk<D, NT, FOLD> s_walk[2 * kWarps];
     float *s_o = reinterpret_cast<float *>(smem + C::kRing);
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const int cta = blockIdx.x;
+    if (tid == 0)
+        s_segments = 0;
+    __syncthreads();
     griddep_wait();
 
-    // ---- this CTA's share of the list
+    // ---- the list of work: how many segments, how long, and this CTA's or warp's share
     const Kv4Seqs &sq = p.a.s;
-    int row0, n, len, nt, nrb;
-    int64_t first = tid < sq.nseq ? sequence<D, NT, FOLD>(p, tid, row0, n, len, nt, nrb) : 0;
-    int64_t total = 0, sum = 0;
+    int row0, n, len, nt0 = 0, nt, nrb, segs0 = 0;
+    for (int i = tid; i < sq.nseq; i += kThreads) {
+        const int segs = sequence<D, NT, FOLD>(p, i, row0, n, len, nt, nrb);
+        if (i == tid) {
+            segs0 = segs;
+            nt0 = nt;
+        }
+        if (segs)
+            atomicAdd(&s_segments, min(segs, kSoloSegments));
+    }
+    __syncthreads();
+    const bool solo = s_segments >= kSoloSegments;
+    const int cost = solo ? kSoloCost : kTeamCost;
+    auto places = [&](int i) -> int64_t {
+        if (i == tid)
+            return (int64_t)segs0 * (nt0 + cost);
+        if (i >= sq.nseq)
+            return 0;
+        const int segs = sequence<D, NT, FOLD>(p, i, row0, n, len, nt, nrb);
+        return (int64_t)segs * (nt + cost);
+    };
+    int64_t total = 0;
     for (int base = 0; base < sq.nseq; base += kThreads) {
-        int64_t v = first, all;
-        if (base)
-            v = base + tid < sq.nseq ? sequence<D, NT, FOLD>(p, base + tid, row0, n, len, nt, nrb) : 0;
-        block_sum_scan(v, s_scan, all);
+        int64_t all;
+        block_sum_scan(places(base + tid), s_scan, all);
         total += all;
     }
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps));
-    const int64_t x0 = cta < ctas ? total * cta / ctas : total;
-    const int64_t x1 = cta < ctas ? total * (cta + 1) / ctas : total;
-    if (x0 >= x1) {
-        if (tid == 0)
-            p.tail[cta].last = -1;
+    const int64_t teams = max((int64_t)1, min((int64_t)gridDim.x * (solo ? kWarps : 1),
+                                              total / (solo ? 1 + kSoloCost : kWarps)));
+    const int team = solo ? cta * kWarps + warp : cta;
+    if (tid <= kWarps) {
+        const int64_t t = solo ? cta * kWarps + tid : cta + (tid > 0);
+        s_x[tid] = t < teams ? total * t / teams : total;
+    }
+    if (cta == 0 && tid == 0)
+        *p.solo = solo;
+    __syncthreads();
+    if (s_x[0] >= s_x[kWarps]) {
+        if (lane == 0 && (solo || warp == 0))
+            p.tail[team].last = -1;
         return;
     }
+    int64_t sum = 0;
     for (int base = 0; base < sq.nseq; base += kThreads) {
-        int64_t v = first, all;
-        if (base)
-            v = base + tid < sq.nseq ? sequence<D, NT, FOLD>(p, base + tid, row0, n, len, nt, nrb) : 0;
-        const int64_t end = sum + block_sum_scan(v, s_scan, all);
-        if (end - v <= x0 && x0 < end) {
-            s_seq = base + tid;
-            s_from = end - v;
-        }
+        int64_t all;
+        const int64_t v = places(base + tid), end = sum + block_sum_scan(v, s_scan, all);
+#pragma unroll
+        for (int w = 0; w < kWarps; w++)
+            if (end - v <= s_x[w] && s_x[w] < end) {
+                s_seq[w] = base + tid;
+                s_from[w] = end - v;
+            }
         sum += all;
     }
     __syncthreads();
     griddep_launch_dependents();
 
-    Walk<D, NT, FOLD> seg, ahead;
-    seg.start(p, x0, x1, s_seq, x0 - s_from);
-    ahead = seg;
+    // the walks live in shared memory: what a warp (solo) or the CTA works on, [0] and in turn
+    // [1] there, then what each warp fetches, which is up to kStages tiles ahead
+    const int step = solo ? 1 : kWarps, place = solo ? 0 : warp;   // of the tiles, this warp's
+    Walk<D, NT, FOLD> *now = s_walk + (solo ? warp : 0);
+    Tail tail{-1, 0, 0, 0, 0};
+    if (lane == 0 && (solo || warp == 0)) {
+        now->live = false;
+        if (s_x[warp] < s_x[warp + 1])
+            now->start(p, cost, s_x[warp], s_x[warp + 1], s_seq[warp], s_x[warp] - s_from[warp]);
+    }
+    __syncthreads();
 
     // ---- the warp's ring of tiles, filled by 16-byte asynchronous copies of all its lanes (a
     // bulk copy per page takes its operands from the warp, not the lane: 15% slower here)
@@ -275,32 +395,47 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
     const int ps = sq.page_size();
     const int64_t page_bytes = kv4_page_bytes(ps, D), page_stride = sq.Hkv * page_bytes;
     const int slice = min(ps, C::kTile);               // keys of a tile that one page holds
+    const int slice_log2 = 31 - __clz(slice);
     // this lane's 16 bytes of a page's first rows (256 / D of a row's codes), and of its
     // params (lanes 0-15 the keys', 16-31 the values')
     constexpr int kRowStep = 1024 / D;                 // rows of codes that 512 bytes hold
     const int code_row = lane / (D / 32), par_row = lane % 16 * (4 / kG);
-    const int64_t par_off = (int64_t)ps * D + (lane / 16) * (ps * kG * 4) + lane % 16 * 16;
-    const uint8_t *head;                               // the segment's head in page 0
-    int next_tile, ids = 0, stage_in = 0;
+    const int par_off = ps * D + (lane / 16) * (ps * kG * 4) + lane % 16 * 16 - lane * 16;
+    const uint8_t *const cache_at = sq.cache + lane * 16;
+    const uint8_t *head;                               // this lane's part of the segment's head in page 0
+    const int32_t *table;                              // of the segment's sequence
+    int next_tile, end_tile, keys, ids = 0, stage_in = 0;
     bool more = true;
+    auto enter = [&](const Walk<D, NT, FOLD> &w) {
+        more = w.live;
+        next_tile = w.t0 + place;
+        end_tile = w.t1;
+        keys = w.len;
+        table = sq.block_table + (int64_t)w.s * sq.max_pages;
+        head = cache_at + w.kvh * page_bytes;
+    };
     // steps to the warp's next tile and looks up its pages (lane i: the i-th), one tile ahead
     // of their use
     auto advance = [&]() {
-        if (next_tile >= ahead.t1) {
+        if (next_tile >= end_tile) {
+            Walk<D, NT, FOLD> w = s_walk[kWarps + warp];
             do {
-                more = more && ahead.next(p);
-                next_tile = ahead.t0 + warp;
-            } while (more && next_tile >= ahead.t1);
-            head = sq.cache + ahead.kvh * page_bytes;
+                w.next(p);
+                enter(w);
+            } while (more && next_tile >= end_tile);
+            __syncwarp();
+            if (lane == 0)
+                s_walk[kWarps + warp] = w;
+            __syncwarp();
         }
         const int key = next_tile * C::kTile + lane * slice;
         ids = 0;
-        if (more && lane * slice < C::kTile && key < ahead.len)
-            ids = __ldg(sq.block_table + (int64_t)ahead.s * sq.max_pages + (key >> sq.page_log2));
+        if (more && lane * slice < C::kTile && key < keys)
+            ids = __ldg(table + (key >> sq.page_log2));
     };
     auto issue = [&]() {
         if (more) {
-            const int k0 = next_tile * C::kTile, left = ahead.len - k0;
+            const int k0 = next_tile * C::kTile, left = keys - k0;
             const uint32_t dst = ring_at + stage_in;
             // a table entry that is no page: its status bit is set and page 0 read in its place
             if ((uint32_t)ids >= (uint32_t)sq.num_pages) {
@@ -308,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 ids = 0;
             }
             __syncwarp();
-            if (slice == C::kTile && left >= C::kTile) {   // a whole tile of one page
+            if (left >= C::kTile && slice == C::kTile) {       // a whole tile of one page
                 const int row = k0 & (ps - 1);
                 const uint8_t *src = head + __shfl_sync(0xffffffffu, ids, 0) * page_stride;
-                const uint8_t *kc = src + row * (D / 2) + lane * 16, *vc = kc + ps * (D / 2);
+                const uint8_t *kc = src + row * (D / 2), *vc = kc + ps * (D / 2);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     copy16(dst + i * 512, kc + i * 512);
@@ -319,114 +454,86 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 }
                 copy16(dst + C::kTile * D, src + par_off + row * (kG * 4));
             } else {
+                // of whole pages (slice < kTile), or the sequence's last rows: copy i holds rows
+                // i kRowStep to (i + 1) kRowStep - 1, all in slice i kRowStep / slice
+                const int row0 = k0 & (ps - 1);                // not 0 only where slice == kTile
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int at = i * kRowStep + code_row;    // at / slice is the same for all lanes
-                    const int id = __shfl_sync(0xffffffffu, ids, i * kRowStep / slice);
-                    const int row = (k0 + at) & (ps - 1);
-                    const uint8_t *kc = head + id * page_stride + row * (D / 2) + lane % (D / 32) * 16;
-                    if (at < left) {
+                    const int id = __shfl_sync(0xffffffffu, ids, i * kRowStep >> slice_log2);
+                    const uint8_t *kc = head + id * page_stride + (row0 + (i * kRowStep & (slice - 1))) * (D / 2);
+                    if (i * kRowStep + code_row < left) {
                         copy16(dst + i * 512, kc);
                         copy16(dst + C::kTile * (D / 2) + i * 512, kc + ps * (D / 2));
                     }
                 }
-                const int id = __shfl_sync(0xffffffffu, ids, par_row / slice);
-                const int row = (k0 + par_row) & (ps - 1);
+                const int id = __shfl_sync(0xffffffffu, ids, par_row >> slice_log2);
                 if (par_row < left)
                     copy16(dst + C::kTile * D, head + id * page_stride + par_off +
-                                                   (row - par_row) * (kG * 4));
+                                                   (row0 - (par_row & ~(slice - 1))) * (kG * 4));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         stage_in = stage_in + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : stage_in + C::kStageBytes;
-        next_tile += kWarps;
+        next_tile += step;
         if (more)
             advance();
     };
-    next_tile = ahead.t0 + warp;
-    head = sq.cache + ahead.kvh * page_bytes;
-    advance();
+    if (lane == 0)
+        s_walk[kWarps + warp] = *now;
+    __syncwarp();
+    enter(*now);
+    if (more)
+        advance();
 #pragma unroll 1
     for (int i = 0; i < C::kStages; i++)
         issue();
     int stage_out = 0;
 
-    int tail_last = -1;
-    Tail tail_info = {-1, 0, 0, 0, 0};
-    bool any = true;
-    while (any) {
+    while (now->live) {
+        const Walk<D, NT, FOLD> &seg = *now;
+        const int end = seg.t1, len = seg.len;
         // ---- the segment's queries: row r of the block is query r / group, head r % group
         const int r0 = seg.rb * C::kRows, nrows = min(C::kRows, seg.n * p.group - r0);
         uint32_t qf[NT][kG][2][4];
         float f[NT][2], qs[NT][kG][2];
         int lim[NT][2];
 #pragma unroll
-        for (int nt8 = 0; nt8 < NT; nt8++) {
-            const int r = FOLD ? g % 4 : nt8 * 8 + g;
-            float x[kG][16], sum[kG];
-            float big = 0.0f;
+        for (int i = 0; i < NT; i++) {
+            const int r = FOLD ? g % 4 : i * 8 + g;
             const int qi = (r0 + r) / p.group, hh = (r0 + r) % p.group;
-            const int64_t off = (int64_t)(seg.row0 + qi) * p.a.q_tok +
-                                (int64_t)(seg.kvh * p.group + hh) * p.a.q_head + t4 * 16;
+            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (int64_t)(seg.row0 + qi) * p.a.q_tok +
+                                  (int64_t)(seg.kvh * p.group + hh) * p.a.q_head + t4 * 16;
+            uint4 u[kG][2];
 #pragma unroll
-            for (int gr = 0; gr < kG; gr++) {
-                float lo8[8] = {}, hi8[8] = {};
-                if (r < nrows) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const uint16_t *>(p.a.q) + off + gr * 64);
-                    const uint4 u = __ldg(src), v = __ldg(src + 1);
-                    if (p.a.bf16) {
-                        load8<__nv_bfloat16>(u, lo8);
-                        load8<__nv_bfloat16>(v, hi8);
-                    } else {
-                        load8<__half>(u, lo8);
-                        load8<__half>(v, hi8);
-                    }
-                }
-                float s = 0.0f;
+            for (int gr = 0; gr < kG; gr++)
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    x[gr][i] = lo8[i];
-                    x[gr][8 + i] = hi8[i];
-                    s += lo8[i] + hi8[i];
-                    big = fmaxf(big, fmaxf(fabsf(lo8[i]), fabsf(hi8[i])));
-                }
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                sum[gr] = s;
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // the row as fp16 with its largest element in [2^14, 2^15): a factor 2^(14 - e)
-            const int e = max(-100, min(100, (int)(__float_as_uint(big) >> 23) - 127));
-            const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            const float unit = __uint_as_float((uint32_t)(127 + 10 + e) << 23);   // 2^(24 - 14 + e)
-            const float back = unit * p.sc_log2;
-            f[nt8][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
-            f[nt8][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
-#pragma unroll
-            for (int gr = 0; gr < kG; gr++) {
-                sum[gr] *= 1.0f / unit;                // exact: a power of two
-                qs[nt8][gr][0] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8);
-                qs[nt8][gr][1] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8 + 4);
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const float *w = x[gr] + 8 * j;
-                    const float s16 = scale * 0.0625f;
-                    qf[nt8][gr][j][0] = pack_half2(w[0] * scale, w[4] * scale);
-                    qf[nt8][gr][j][1] = pack_half2(w[1] * s16, w[5] * s16);
-                    qf[nt8][gr][j][2] = pack_half2(w[2] * scale, w[6] * scale);
-                    qf[nt8][gr][j][3] = pack_half2(w[3] * s16, w[7] * s16);
-                }
-            }
+                for (int j = 0; j < 2; j++)
+                    u[gr][j] = r < nrows ? __ldg(reinterpret_cast<const uint4 *>(src + gr * 64) + j)
+                                         : make_uint4(0u, 0u, 0u, 0u);
+            f[i][0] = f[i][1] = query_row<kG>(u, p.a.bf16, qf[i]);
+            f[i][0] = __shfl_sync(0xffffffffu, f[i][0], t4 * 8) * p.sc_log2;
+            f[i][1] = __shfl_sync(0xffffffffu, f[i][1], t4 * 8 + 4) * p.sc_log2;
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                const int rr = FOLD ? (2 * t4 + c) % 4 : nt8 * 8 + 2 * t4 + c;
-                lim[nt8][c] = p.a.causal && rr < nrows ? seg.len - seg.n + (r0 + rr) / p.group : seg.len - 1;
+                const int rr = FOLD ? (2 * t4 + c) % 4 : i * 8 + 2 * t4 + c;
+                lim[i][c] = p.a.causal && rr < nrows ? len - seg.n + (r0 + rr) / p.group : len - 1;
+            }
+            // a row's sum over a group's channels, in the products' own units: codes that are all 1
+#pragma unroll
+            for (int gr = 0; gr < kG; gr++) {
+                float one[4] = {};
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++)
+                        mma16816(one, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qf[i][gr][j][2 * hf],
+                                 qf[i][gr][j][2 * hf + 1]);
+                qs[i][gr][0] = one[0];
+                qs[i][gr][1] = one[1];
             }
         }
         // keys up to here are seen by every row of the block
-        const int seen = p.a.causal ? min(seg.len - 1, seg.len - seg.n + r0 / p.group) : seg.len - 1;
+        const int seen = p.a.causal ? min(len - 1, len - seg.n + r0 / p.group) : len - 1;
 
         float nm[NT][2], l[NT][2], o2[NT][kG][2], o[NT][kG][4][4];   // nm: -m
 #pragma unroll
@@ -449,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
         const float2 low_sel = t4 < 2 ? make_float2(0.0f, 0.0f) : make_float2(-1.0f, -1.0f);
         int vexp = -64;                                // exponent the value products are scaled for
 
-        for (int t = seg.t0 + warp; t < seg.t1; t += kWarps) {
+        for (int t = seg.t0 + place; t < end; t += step) {
             const int k0 = t * C::kTile;
             const uint8_t *st = ring + stage_out;
             asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
@@ -532,9 +639,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             vs.x &= 0x7FFFu;
             vs.y &= 0x7FFFu;
             if (masked) {
-                if (vs.x >= 0x7C00u || k0 + 2 * lane / kG >= seg.len)
+                if (vs.x >= 0x7C00u || k0 + 2 * lane / kG >= len)
                     vs.x = 0;
-                if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= seg.len)
+                if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= len)
                     vs.y = 0;
             }
             const int texp = (int)(__reduce_max_sync(0xffffffffu, max(vs.x, vs.y)) >> 10);
@@ -666,23 +773,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             issue();
         }
 
-        // ---- merge the warps: maximum, weight and sums of each row through shared memory
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
+        if (!whole && seg.t0 == 0) {
+            // the list's place behind the segment's last tile lies in the share of team
+            // ceil(place teams / total) - 1
+            const int64_t last = seg.x + cost + seg.nt;
+            tail = Tail{(int)((last * teams + total - 1) / total) - 1, seg.row0, seg.n, seg.kvh, seg.rb};
+        }
         const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 - 18 + vexp) << 23);
+        float *const part = p.part + (int64_t)(team * 2 + (seg.t0 == 0)) * (C::kRows * C::kPitch);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 const int r = FOLD ? (2 * t4 + c) % 4 : i * 8 + 2 * t4 + c;
                 float lw = l[i][c], ow[kG];
-                if (FOLD) {                            // high and low terms' columns
-#pragma unroll
-                    for (int gr = 0; gr < kG; gr++)
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            o[i][gr][j][c] += __shfl_xor_sync(0xffffffffu, o[i][gr][j][c], 2);
-                            o[i][gr][j][c + 2] += __shfl_xor_sync(0xffffffffu, o[i][gr][j][c + 2], 2);
-                        }
-                }
 #pragma unroll
                 for (int gr = 0; gr < kG; gr++)
                     ow[gr] = o2[i][gr][c];
@@ -693,120 +798,184 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                     for (int gr = 0; gr < kG; gr++)
                         ow[gr] += __shfl_xor_sync(0xffffffffu, ow[gr], x);
                 }
-                if (g == 0) {
-                    s_m[warp][r] = -nm[i][c];
-                    s_l[warp][r] = lw;
-                }
-                if (r < nrows && !(FOLD && t4 >= 2)) {
-                    float *dst = s_o + (warp * C::kRows + r) * C::kPitch + g * 8;
+                // FOLD: the low terms' columns (t4 >= 2) join the high ones'
+                float v[kG][8];
+#pragma unroll
+                for (int gr = 0; gr < kG; gr++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            float y = o[i][gr][j][c + 2 * e];
+                            if (FOLD)
+                                y += __shfl_xor_sync(0xffffffffu, y, 2);
+                            v[gr][2 * j + e] = fmaf(y, unscale, ow[gr]);
+                        }
+                if (r >= nrows || (FOLD && t4 >= 2))
+                    continue;
+                if (solo && whole) {
+                    const float inv = lw == 0.0f ? 0.0f : 1.0f / lw;
+                    const int64_t row = seg.row0 + (r0 + r) / p.group;
+                    const int hh = seg.kvh * p.group + (r0 + r) % p.group;
+                    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row * p.a.Hq + hh) * D + g * 8;
+#pragma unroll
+                    for (int gr = 0; gr < kG; gr++) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            v[gr][e] *= inv;
+                        *reinterpret_cast<uint4 *>(out + gr * 64) =
+                            p.a.bf16 ? store8<__nv_bfloat16>(v[gr]) : store8<__half>(v[gr]);
+                    }
+                    if (g == 0 && p.a.lse)
+                        p.a.lse[row * p.a.Hq + hh] = lw == 0.0f ? -INFINITY : (log2f(lw) - nm[i][c]) * kLn2;
+                } else {
+                    // to the workspace, or (CTA) to shared memory, where the warps are merged
+                    float *dst = solo ? part + r * C::kPitch : s_o + (warp * C::kRows + r) * C::kPitch;
 #pragma unroll
                     for (int gr = 0; gr < kG; gr++)
 #pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            *reinterpret_cast<float2 *>(dst + gr * 64 + 2 * j) =
-                                make_float2(fmaf(o[i][gr][j][c], unscale, ow[gr]),
-                                            fmaf(o[i][gr][j][c + 2], unscale, ow[gr]));
+                        for (int h = 0; h < 2; h++)
+                            *reinterpret_cast<float4 *>(dst + gr * 64 + g * 8 + 4 * h) =
+                                make_float4(v[gr][4 * h], v[gr][4 * h + 1], v[gr][4 * h + 2], v[gr][4 * h + 3]);
+                    if (g == 0)
+                        *reinterpret_cast<float2 *>(dst + D) = make_float2(-nm[i][c], lw);
                 }
             }
         }
+        if (solo) {
+            __syncwarp();
+            if (lane == 0)
+                now->next(p);
+            __syncwarp();
+            continue;
+        }
         __syncthreads();
-        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
+        Walk<D, NT, FOLD> *const then = s_walk + (now == s_walk);
+        if (tid == kThreads - 1) {
+            *then = seg;
+            then->next(p);
+        }
         for (int e = tid; e < nrows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), c4 = e % (D / 4) * 4;
+            const float *at = s_o + r * C::kPitch;
             float M = -INFINITY, L = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; w++)
-                M = fmaxf(M, s_m[w][r]);
+                M = fmaxf(M, at[w * C::kRows * C::kPitch + D]);
             const float b = M == -INFINITY ? 0.0f : M;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kWarps; w++) {
-                const float wt = ex2_approx(s_m[w][r] - b);
-                const float4 v = *reinterpret_cast<const float4 *>(s_o + (w * C::kRows + r) * C::kPitch + c4);
-                L = fmaf(wt, s_l[w][r], L);
+                const float *x = at + w * C::kRows * C::kPitch;
+                const float2 ml = *reinterpret_cast<const float2 *>(x + D);
+                const float4 v = *reinterpret_cast<const float4 *>(x + c4);
+                const float wt = ex2_approx(ml.x - b);
+                L = fmaf(wt, ml.y, L);
                 acc.x = fmaf(wt, v.x, acc.x);
                 acc.y = fmaf(wt, v.y, acc.y);
                 acc.z = fmaf(wt, v.z, acc.z);
                 acc.w = fmaf(wt, v.w, acc.w);
             }
             if (whole) {
-                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                 const int64_t row = seg.row0 + (r0 + r) / p.group;
-                const int head = seg.kvh * p.group + (r0 + r) % p.group;
-                const int64_t at = (row * p.a.Hq + head) * D + c4;
-                uint2 u;
-                if (p.a.bf16) {
-                    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
-                    h[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-                    h[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                } else {
-                    u.x = pack_half2(acc.x * inv, acc.y * inv);
-                    u.y = pack_half2(acc.z * inv, acc.w * inv);
-                }
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + at) = u;
-                if (c4 == 0 && p.a.lse)
-                    p.a.lse[row * p.a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+                write_row<4>(p.a, row, seg.kvh * p.group + (r0 + r) % p.group, D, c4, M, L,
+                             reinterpret_cast<const float *>(&acc));
             } else {
-                float *part = p.part + ((int64_t)(cta * 2 + (seg.t0 == 0)) * C::kRows + r) * (D + 2);
-                *reinterpret_cast<float2 *>(part + c4) = make_float2(acc.x, acc.y);
-                *reinterpret_cast<float2 *>(part + c4 + 2) = make_float2(acc.z, acc.w);
-                if (c4 == 0) {
-                    part[D] = M;
-                    part[D + 1] = L;
-                }
+                *reinterpret_cast<float4 *>(part + r * C::kPitch + c4) = acc;
+                if (c4 == 0)
+                    *reinterpret_cast<float2 *>(part + r * C::kPitch + D) = make_float2(M, L);
             }
         }
-        if (!whole && seg.t0 == 0) {
-            // the list's position behind the segment's last tile lies in the share of CTA
-            // ceil(end ctas / total) - 1
-            const int64_t end = seg.x + seg.nt;
-            tail_info = Tail{(int)((end * ctas + total - 1) / total) - 1, seg.row0, seg.n, seg.kvh, seg.rb};
-            tail_last = tail_info.last;
-        }
-        any = seg.next(p);
         __syncthreads();                               // the merge buffer is free again
+        now = then;
     }
-    if (tid == 0) {
-        tail_info.last = tail_last;
-        p.tail[cta] = tail_info;
-    }
+    if (lane == 0 && (solo || warp == 0))
+        p.tail[team] = tail;
 }
 
-// Merge of what several CTAs share: CTA (c, r) takes row r of the segment that CTA c began.
+// Merge of what several teams share: CTA t takes the segment that team t began and did not
+// finish. Its warps take the rows, several a row where the rows are few, eight partials at a
+// time (all their loads in flight together), always in the same order.
 template <int D, int NT, bool FOLD>
-__global__ void __launch_bounds__(D) kv4_attn_merge(const Params p)
+__global__ void __launch_bounds__(kThreads) kv4_attn_merge(const Params p)
 {
     using C = Cfg<D, NT, FOLD>;
+    constexpr int kC = D / 32, kChunk = 8;             // channels of a lane, partials at a time
+    __shared__ __align__(16) float s_part[kWarps][D];
+    __shared__ float2 s_ml[kWarps];
     griddep_wait();
-    const int c0 = blockIdx.x, r = blockIdx.y, ch = threadIdx.x;
-    const Tail t = p.tail[c0];
-    const int rr = t.rb * C::kRows + r;
-    if (t.last < 0 || rr >= t.n * p.group)
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, team = blockIdx.x;
+    if (*p.solo == 0 && team >= gridDim.x / kWarps)
         return;
-    auto slot = [&](int c) {
-        return p.part + ((int64_t)(c * 2 + (c == c0)) * C::kRows + r) * (D + 2);
-    };
-    float M = -INFINITY;
-    for (int c = c0; c <= t.last; c++)
-        M = fmaxf(M, slot(c)[D]);
-    const float b = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f, O = 0.0f;
-    for (int c = c0; c <= t.last; c++) {
-        const float *s = slot(c);
-        const float w = ex2_approx(s[D] - b);
-        L = fmaf(w, s[D + 1], L);
-        O = fmaf(w, s[ch], O);
+    const Tail t = p.tail[team];
+    if (t.last < 0)
+        return;
+    const int r0 = t.rb * C::kRows, nrows = min(C::kRows, t.n * p.group - r0);
+    const int split = nrows <= 1 ? 8 : nrows <= 2 ? 4 : nrows <= 4 ? 2 : 1;   // warps of a row
+    const int each = (t.last - team + split) / split, part = warp % split;
+    const int c0 = team + part * each, c1 = min(t.last + 1, c0 + each);
+    for (int base = 0; base < nrows; base += kWarps / split) {
+        const int r = base + warp / split;
+        float M = -INFINITY, L = 0.0f, acc[kC] = {};
+        for (int c = c0; r < nrows && c < c1; c += kChunk) {
+            float2 ml[kChunk];
+            float v[kChunk][kC];
+#pragma unroll
+            for (int i = 0; i < kChunk; i++) {
+                const bool in = c + i < c1;
+                const float *x = p.part + ((int64_t)((in ? c + i : c) * 2 + (c + i == team)) * C::kRows + r) * C::kPitch;
+                ml[i] = *reinterpret_cast<const float2 *>(x + D);
+                if (!in)
+                    ml[i] = make_float2(-INFINITY, 0.0f);
+                if constexpr (kC == 4) {
+                    *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(x + lane * 4);
+                } else {
+                    *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(x + lane * 2);
+                }
+            }
+            float m = M;
+#pragma unroll
+            for (int i = 0; i < kChunk; i++)
+                m = fmaxf(m, ml[i].x);
+            const float b = m == -INFINITY ? 0.0f : m, scale = ex2_approx(M - b);
+            M = m;
+            L *= scale;
+#pragma unroll
+            for (int k = 0; k < kC; k++)
+                acc[k] *= scale;
+#pragma unroll
+            for (int i = 0; i < kChunk; i++) {
+                const float w = ex2_approx(ml[i].x - b);
+                L = fmaf(w, ml[i].y, L);
+#pragma unroll
+                for (int k = 0; k < kC; k++)           // a slot read in place of one past the end: no part
+                    acc[k] = fmaf(w, c + i < c1 ? v[i][k] : 0.0f, acc[k]);
+            }
+        }
+        if (split > 1) {
+            __syncthreads();
+            s_ml[warp] = make_float2(M, L);
+#pragma unroll
+            for (int k = 0; k < kC; k++)
+                s_part[warp][lane * kC + k] = acc[k];
+            __syncthreads();
+            if (part)
+                continue;
+            for (int w = warp + 1; w < warp + split; w++) {
+                const float2 o = s_ml[w];
+                const float m = fmaxf(M, o.x), b = m == -INFINITY ? 0.0f : m;
+                const float sa = ex2_approx(M - b), sb = ex2_approx(o.x - b);
+                M = m;
+                L = fmaf(sb, o.y, sa * L);
+#pragma unroll
+                for (int k = 0; k < kC; k++)
+                    acc[k] = fmaf(sb, s_part[w][lane * kC + k], sa * acc[k]);
+            }
+        }
+        if (r < nrows)
+            write_row<kC>(p.a, t.row0 + (r0 + r) / p.group, t.kvh * p.group + (r0 + r) % p.group, D, lane * kC, M, L,
+                          acc);
     }
-    const int64_t row = t.row0 + rr / p.group;
-    const int head = t.kvh * p.group + rr % p.group;
-    const int64_t at = (row * p.a.Hq + head) * D + ch;
-    const float v = L == 0.0f ? 0.0f : O / L;
-    if (p.a.bf16)
-        static_cast<__nv_bfloat16 *>(p.a.out)[at] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half *>(p.a.out)[at] = __float2half_rn(v);
-    if (ch == 0 && p.a.lse)
-        p.a.lse[row * p.a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // What takes a call's rows per key head: the folded tile up to 4, one tile up to 8, else two.
@@ -830,27 +999,27 @@ cudaError_t launch(const Params &p, cudaStream_t st)
     kv4_attn_kernel<D, NT, FOLD><<<n, kThreads, C::kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const int rows = std::min(C::kRows, p.a.max_q * p.group);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n, rows);
-    cfg.blockDim = dim3(D);
+    cfg.gridDim = dim3(n * kWarps);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kv4_attn_merge<D, NT, FOLD>, p);
 }
 
-size_t tail_bytes(int var) { return (sizeof(Tail) * ctas(var) + 255) / 256 * 256; }
+// [whether solo | tails], then the partial rows, of as many teams as there are warps
+size_t tail_bytes(int var) { return (256 + sizeof(Tail) * kWarps * ctas(var) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t kv4_attn_workspace(int Hq, int Hkv, int max_q, int d)
 {
     const int var = variant(Hq, Hkv, max_q);
-    return tail_bytes(var) + (size_t)ctas(var) * 2 * rows_of(var) * (d + 2) * sizeof(float);
+    return tail_bytes(var) + (size_t)kWarps * ctas(var) * 2 * rows_of(var) * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t st)
@@ -858,7 +1027,8 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t st)
     const int var = variant(a.Hq, a.s.Hkv, a.max_q);
     Params p;
     p.a = a;
-    p.tail = static_cast<Tail *>(a.workspace);
+    p.solo = static_cast<int *>(a.workspace);
+    p.tail = reinterpret_cast<Tail *>(static_cast<char *>(a.workspace) + 256);
     p.part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + tail_bytes(var));
     p.group = a.Hq / a.s.Hkv;
     p.sc_log2 = a.sm_scale * kLog2e;
