@@ -5,6 +5,7 @@
 // them. Gather is the way back: tokens of the cache as 16-bit tensors. Both read and write
 // every byte once and are bound by HBM when the tokens are many, by latency when few.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "quant_codes.cuh"
@@ -89,205 +90,305 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// Codes of eight channels, channel i in bits 4i .. 4i+3. round((x - low) / step) with the
-// product by r = fl(1 / step) in place of the quotient: clamped to [-1, 16] first, the two
-// differ by less than 2^-17, so they round alike unless the product is within 2^-15 of a
-// half-integer; those take the division itself.
+__device__ __forceinline__ float min_nan(float a, float b, float c)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Least and greatest of eight.
+__device__ __forceinline__ float min8(const float (&x)[8])
+{
+    return min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[7]));
+}
+__device__ __forceinline__ float max8(const float (&x)[8])
+{
+    return max_nan(max_nan(x[0], x[1], x[2]), max_nan(x[3], x[4], x[5]), max_nan(x[6], x[7]));
+}
+
+// Codes of eight channels, channel i in bits 4i .. 4i+3: round((x - low) / step), clamped. The
+// product with r = fl(1 / step) stands in for the quotient: where it is below 16 the two differ
+// by less than 2^-17, so they round alike unless the product is within 2^-15 of a half-integer;
+// then the division itself is taken (2^-14 of the elements). Adding 1.5 2^23 rounds to an
+// integer in the low bits of the sum; the constant parts of eight such sums are taken off the
+// packed word together.
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float step, float low, float r)
 {
     if (step == 0.0f)
         return 0u;
+    float d[8], b[8], far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 e = add2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(-low, -low));
+        const float2 q = mul2(e, make_float2(r, r));
+        const float2 n = add2(q, make_float2(kRound, kRound));
+        const float2 t = fma2(add2(n, make_float2(-kRound, -kRound)), make_float2(-1.0f, -1.0f), q);
+        d[2 * i] = e.x;
+        d[2 * i + 1] = e.y;
+        b[2 * i] = n.x;
+        b[2 * i + 1] = n.y;
+        far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
+    }
+    if (far > 0.5f - 3.0517578125e-05f) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            b[i] = kRound + rintf(fminf(fmaxf(__fdiv_rn(d[i], step), -1.0f), 16.0f));
+    }
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float d = __fsub_rn(x[i], low);
-        const float q = fminf(fmaxf(d * r, -1.0f), 16.0f);
-        float n = rintf(q);
-        if (fabsf(q - n) > 0.5f - 3.0517578125e-05f)
-            n = rintf(__fdiv_rn(d, step));
-        w |= (uint32_t)max(0, min(15, __float2int_rn(n))) << (4 * i);
-    }
-    return w;
+    for (int i = 7; i >= 0; i--)                       // a NaN becomes the lower bound: code 0
+        w = (w << 4) + __float_as_uint(fminf(fmaxf(b[i], kRound), kRound + 15.0f));
+    return w - (uint32_t)kRoundBits * 0x11111111u;
 }
 
-// One CTA: a few tokens. Threads first rotate the queries, 16 channels each; then d/16
-// neighbouring lanes take one head of keys or values (the keys rotated like the queries),
-// reduce the groups' extremes over their lanes and write the codes.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArgs p, int tokens_per_cta,
-                                                              int q_ctas)
+// A thread keeps one place of one token, 16 channels (unit u), and walks over the heads of its
+// CTA, a slice (blockIdx.y) of the queries' and of the keys' and values'. Its first rows are
+// under way while the tokens' places, sines and cosines are worked out, each next one while one
+// is computed. Keys and values: the d/16 neighbouring lanes of a head reduce their groups'
+// extremes together and write the codes.
+template <typename T, int D, int TOKENS>
+__global__ void __launch_bounds__(kThreads, TOKENS == 1 ? 2 : 3) kv4_append_kernel(const Kv4AppendArgs p, int q_heads, int kv_heads)
 {
-    constexpr int kUnits = D / 16, kGroups = D / kKv4Group;
-    __shared__ float2 s_cs[2 * kThreads];             // [tokens][rot / 2]
+    constexpr int kUnits = D / 16, kGroups = D / kKv4Group, kStep = kThreads / (TOKENS * kUnits);
+    // cosines and sines, [TOKENS][rot / 2]
+    __shared__ __align__(16) float s_c[TOKENS * D / 2], s_s[TOKENS * D / 2];
     __shared__ Places s_w;
     griddep_wait();
-    const int t0 = blockIdx.x * tokens_per_cta;
-    const int tokens = min(tokens_per_cta, p.s.total - t0);
+    const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, p.s.total - t0);
     const int64_t page_bytes = kv4_page_bytes(p.s.page_size(), D);
+    const int u = threadIdx.x % kUnits, tl = threadIdx.x / kUnits % TOKENS, hl = threadIdx.x / (kUnits * TOKENS);
+    const bool here = tl < tokens;
+    const int t = t0 + tl;
+    const int q0 = blockIdx.y * q_heads, q1 = p.q ? min(p.Hq, q0 + q_heads) : 0;
+    const int k0 = blockIdx.y * kv_heads, k1 = min(p.s.Hkv, k0 + kv_heads);
+    const RopeUnit ru = rope_unit(u, p.rot, p.interleaved), vu = rope_unit(u, 0, 0);
+    uint4 wq[2], wk[2], wv[2];
+    auto load = [&](uint4 (&w)[2], const void *x, int64_t tok, int64_t head, int h, const RopeUnit &unit) {
+        const T *in = static_cast<const T *>(x) + t * tok + h * head;
+        w[0] = *reinterpret_cast<const uint4 *>(in + unit.a0);
+        w[1] = *reinterpret_cast<const uint4 *>(in + unit.a1);
+    };
+    if (here && q0 + hl < q1)
+        load(wq, p.q, p.q_tok, p.q_head, q0 + hl, ru);
+    if (here && k0 + hl < k1) {
+        load(wk, p.k, p.k_tok, p.k_head, k0 + hl, ru);
+        load(wv, p.v, p.v_tok, p.v_head, k0 + hl, vu);
+    }
     find_places(p.s, t0, tokens, page_bytes, s_w);
     __syncthreads();
     const int half = p.rot / 2;
-    for (int i = threadIdx.x; i < tokens * half; i += kThreads)
-        s_cs[i] = rope_cos_sin(s_w.pos[i / half], __ldg(p.freqs + i % half), p.mscale, false);
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int k = i / half;
+        const float2 cs = rope_cos_sin(s_w.pos[k], __ldg(p.freqs + (i - k * half)), p.mscale, false);
+        s_c[i] = cs.x;
+        s_s[i] = cs.y;
+    }
     __syncthreads();
+    RopeAngles cs;
+    if (ru.rotated && here)
+        cs.load(s_c + tl * half + 8 * u, s_s + tl * half + 8 * u);
 
-    if ((int)blockIdx.y < q_ctas) {
-        const int hpc = (p.Hq + q_ctas - 1) / q_ctas, h0 = blockIdx.y * hpc;
-        const int nh = min(hpc, p.Hq - h0);
-        for (int i = threadIdx.x; i < tokens * nh * kUnits; i += kThreads) {
-            const int u = i % kUnits, h = h0 + i / kUnits % nh, tl = i / (kUnits * nh);
-            if (s_w.pos[tl] < 0)
-                continue;
-            const T *in = static_cast<const T *>(p.q) + (t0 + tl) * p.q_tok + h * p.q_head;
-            T *out = static_cast<T *>(p.q_out) + (t0 + tl) * p.qo_tok + h * p.qo_head;
-            const RopeUnit ru = rope_unit(u, p.rot, p.interleaved);
-            uint4 w0 = *reinterpret_cast<const uint4 *>(in + ru.a0);
-            uint4 w1 = *reinterpret_cast<const uint4 *>(in + ru.a1);
+    if (here && s_w.pos[tl] >= 0) {
+        for (int h = q0 + hl; h < q1; h += kStep) {
+            uint4 w0 = wq[0], w1 = wq[1];
+            if (h + kStep < q1)
+                load(wq, p.q, p.q_tok, p.q_head, h + kStep, ru);
             if (ru.rotated) {
                 float f0[8], f1[8];
                 load8<T>(w0, f0);
                 load8<T>(w1, f1);
-                rope_rotate(f0, f1, s_cs + tl * half + 8 * u, p.interleaved);
+                rope_rotate(f0, f1, cs, p.interleaved);
                 w0 = store8<T>(f0);
                 w1 = store8<T>(f1);
             }
+            T *out = static_cast<T *>(p.q_out) + t * p.qo_tok + h * p.qo_head;
             *reinterpret_cast<uint4 *>(out + ru.a0) = w0;
             *reinterpret_cast<uint4 *>(out + ru.a1) = w1;
         }
     }
-    if (blockIdx.y + 1 != gridDim.y)
-        return;
-    const int items = tokens * 2 * p.s.Hkv * kUnits;
-    const int whole = (items + 31) / 32 * 32;         // whole warps reach the shuffles
-    for (int i = threadIdx.x; i < whole; i += kThreads) {
-        const int u = i % kUnits, hv = i / kUnits % (2 * p.s.Hkv);
-        const int tl = i / (kUnits * 2 * p.s.Hkv);
-        const bool is_v = hv >= p.s.Hkv;
-        const int h = is_v ? hv - p.s.Hkv : hv;
-        const bool on = i < items && s_w.base[min(tl, tokens - 1)] >= 0;
-        const RopeUnit ru = rope_unit(u, is_v ? 0 : p.rot, p.interleaved);
-        float f0[8] = {}, f1[8] = {};
-        if (on) {
-            const T *in = is_v ? static_cast<const T *>(p.v) + (t0 + tl) * p.v_tok + h * p.v_head
-                               : static_cast<const T *>(p.k) + (t0 + tl) * p.k_tok + h * p.k_head;
-            load8<T>(*reinterpret_cast<const uint4 *>(in + ru.a0), f0);
-            load8<T>(*reinterpret_cast<const uint4 *>(in + ru.a1), f1);
-            if (ru.rotated)
-                rope_rotate(f0, f1, s_cs + tl * half + 8 * u, p.interleaved);
-            if (!is_v && p.k_mean) {
-                const float *m = p.k_mean + h * D;
+    const bool on = here && s_w.base[min(tl, tokens - 1)] >= 0;
+    const int ps = p.s.page_size(), row = here ? s_w.pos[tl] & (ps - 1) : 0;
+    uint8_t *const at = p.s.cache + (on ? s_w.base[tl] : 0);
+    // keys, then values; whole warps reach the shuffles
+    auto walk = [&](auto values, uint4 (&w)[2], const void *x, int64_t tok, int64_t head) {
+        constexpr bool is_v = decltype(values)::value;
+        const RopeUnit &unit = is_v ? vu : ru;
+        const int a0 = unit.a0, a1 = unit.a1;
+        for (int top = hl / (32 / kUnits) * (32 / kUnits); k0 + top < k1; top += kStep) {
+            const int h = k0 + top + hl % (32 / kUnits);
+            const bool act = on && h < k1;
+            float f0[8] = {}, f1[8] = {};
+            if (act) {
+                load8<T>(w[0], f0);
+                load8<T>(w[1], f1);
+                if (h + kStep < k1)
+                    load(w, x, tok, head, h + kStep, unit);
+            }
+            if (act && !is_v) {
+                if (ru.rotated)
+                    rope_rotate(f0, f1, cs, p.interleaved);
+                if (p.k_mean) {
+                    const float2 *m0 = reinterpret_cast<const float2 *>(p.k_mean + h * D + a0);
+                    const float2 *m1 = reinterpret_cast<const float2 *>(p.k_mean + h * D + a1);
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    f0[j] = __fsub_rn(f0[j], __ldg(m + ru.a0 + j));
-                    f1[j] = __fsub_rn(f1[j], __ldg(m + ru.a1 + j));
+                    for (int j = 0; j < 4; j++) {
+                        const float2 x = sub2(make_float2(f0[2 * j], f0[2 * j + 1]), __ldg(m0 + j));
+                        const float2 y = sub2(make_float2(f1[2 * j], f1[2 * j + 1]), __ldg(m1 + j));
+                        f0[2 * j] = x.x;
+                        f0[2 * j + 1] = x.y;
+                        f1[2 * j] = y.x;
+                        f1[2 * j + 1] = y.y;
+                    }
                 }
             }
-        }
-        // extremes of each group over the head's lanes
-        float lo[kGroups], hi[kGroups];
-        {
-            float l0 = f0[0], x0 = f0[0], l1 = f1[0], x1 = f1[0];
+            // extremes of the groups of this lane's two chunks, over the lanes that share them:
+            // values have both chunks in one group, four lanes a group
+            float lo0 = min8(f0), hi0 = max8(f0), lo1 = min8(f1), hi1 = max8(f1);
+            if constexpr (is_v) {
+                lo0 = min_nan(lo0, lo1);
+                hi0 = max_nan(hi0, hi1);
 #pragma unroll
-            for (int j = 1; j < 8; j++) {
-                l0 = min_nan(l0, f0[j]);
-                x0 = max_nan(x0, f0[j]);
-                l1 = min_nan(l1, f1[j]);
-                x1 = max_nan(x1, f1[j]);
-            }
-#pragma unroll
-            for (int g = 0; g < kGroups; g++) {
-                const bool in0 = ru.a0 / kKv4Group == g, in1 = ru.a1 / kKv4Group == g;
-                lo[g] = min_nan(in0 ? l0 : INFINITY, in1 ? l1 : INFINITY);
-                hi[g] = max_nan(in0 ? x0 : -INFINITY, in1 ? x1 : -INFINITY);
-#pragma unroll
-                for (int o = kUnits / 2; o > 0; o >>= 1) {
-                    lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
-                    hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
+                for (int o = 2; o > 0; o >>= 1) {
+                    lo0 = min_nan(lo0, __shfl_xor_sync(0xffffffffu, lo0, o));
+                    hi0 = max_nan(hi0, __shfl_xor_sync(0xffffffffu, hi0, o));
                 }
+                lo1 = lo0;
+                hi1 = hi0;
+            } else {
+                float lo[kGroups], hi[kGroups];
+#pragma unroll
+                for (int g = 0; g < kGroups; g++) {
+                    const bool in0 = a0 / kKv4Group == g, in1 = a1 / kKv4Group == g;
+                    lo[g] = min_nan(in0 ? lo0 : INFINITY, in1 ? lo1 : INFINITY);
+                    hi[g] = max_nan(in0 ? hi0 : -INFINITY, in1 ? hi1 : -INFINITY);
+#pragma unroll
+                    for (int o = kUnits / 2; o > 0; o >>= 1) {
+                        lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
+                        hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
+                    }
+                }
+                const bool s0 = kGroups > 1 && a0 / kKv4Group, s1 = kGroups > 1 && a1 / kKv4Group;
+                lo0 = s0 ? lo[kGroups - 1] : lo[0];
+                hi0 = s0 ? hi[kGroups - 1] : hi[0];
+                lo1 = s1 ? lo[kGroups - 1] : lo[0];
+                hi1 = s1 ? hi[kGroups - 1] : hi[0];
             }
+            if (!act)
+                continue;
+            uint8_t *page = at + h * page_bytes;
+            uint8_t *codes = page + (is_v ? ps * (D / 2) : 0) + row * (D / 2);
+            __half2 *params = reinterpret_cast<__half2 *>(page + ps * D + (is_v ? ps * kGroups * 4 : 0)) +
+                              row * kGroups;
+            auto store = [&](const float (&f)[8], int a, float lo, float hi) {
+                const __half step = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
+                const __half low = __float2half_rn(lo);
+                const float sf = __half2float(step);
+                *reinterpret_cast<uint32_t *>(codes + a / 2) = codes8(f, sf, __half2float(low), __frcp_rn(sf));
+                if (a % kKv4Group == 0)                // the chunk that begins a group writes its params
+                    params[a / kKv4Group] = __halves2half2(step, low);
+            };
+            store(f0, a0, lo0, hi0);
+            store(f1, a1, lo1, hi1);
         }
-        if (!on)
-            continue;
-        __half step[kGroups], low[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; g++) {
-            step[g] = __float2half_rn(__fmul_rn(__fsub_rn(hi[g], lo[g]), 1.0f / 15.0f));
-            low[g] = __float2half_rn(lo[g]);
-        }
-        const int ps = p.s.page_size(), row = s_w.pos[tl] & (ps - 1);
-        uint8_t *page = p.s.cache + s_w.base[tl] + h * page_bytes;
-        uint8_t *codes = page + (is_v ? ps * (D / 2) : 0) + row * (D / 2);
-        __half2 *params = reinterpret_cast<__half2 *>(page + ps * D + (is_v ? ps * kGroups * 4 : 0)) +
-                          row * kGroups;
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-            const int a = c ? ru.a1 : ru.a0;
-            const int g = kGroups == 1 ? 0 : a / kKv4Group;
-            const float sf = __half2float(kGroups > 1 && g ? step[kGroups - 1] : step[0]);
-            const float lf = __half2float(kGroups > 1 && g ? low[kGroups - 1] : low[0]);
-            *reinterpret_cast<uint32_t *>(codes + a / 2) = codes8(c ? f1 : f0, sf, lf, __frcp_rn(sf));
-        }
-        if (u < kGroups)
-            params[u] = __halves2half2(u ? step[kGroups - 1] : step[0], u ? low[kGroups - 1] : low[0]);
-    }
+    };
+    walk(std::false_type{}, wk, p.k, p.k_tok, p.k_head);
+    walk(std::true_type{}, wv, p.v, p.v_tok, p.v_head);
 }
 
-// One CTA: a few tokens; a thread turns one 32-bit word of codes (8 channels) into 16 bytes.
+// One CTA: a few tokens. A thread keeps one 32-bit word of codes (8 channels) and walks over the
+// tokens' heads, keys and values together.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4GatherArgs p, int tokens_per_cta)
 {
-    constexpr int kWords = D / 8, kGroups = D / kKv4Group;
+    constexpr int kWords = D / 8, kGroups = D / kKv4Group, kStep = kThreads / kWords, kUnroll = 2;
     __shared__ Places s_w;
     griddep_wait();
     const int t0 = blockIdx.x * tokens_per_cta;
     const int tokens = min(tokens_per_cta, p.s.total - t0);
-    const int ps = p.s.page_size();
+    const int ps = p.s.page_size(), Hkv = p.s.Hkv;
     const int64_t page_bytes = kv4_page_bytes(ps, D);
     find_places(p.s, t0, tokens, page_bytes, s_w);
     __syncthreads();
-    const int items = tokens * p.s.Hkv * kWords;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int wd = i % kWords, h = i / kWords % p.s.Hkv, tl = i / (kWords * p.s.Hkv);
-        if (s_w.base[tl] < 0)
-            continue;
-        const int row = s_w.pos[tl] & (ps - 1);
-        const uint8_t *page = p.s.cache + s_w.base[tl] + h * page_bytes;
-        const int64_t o = ((int64_t)(t0 + tl) * p.s.Hkv + h) * p.rep * D + wd * 8;
+    const int wd = threadIdx.x % kWords;
+    const int dt = kStep / Hkv, dh = kStep % Hkv;      // a step to the thread's next (token, head)
+    int tl = threadIdx.x / kWords / Hkv, h = threadIdx.x / kWords % Hkv;
+    while (tl < tokens) {
+        uint32_t w[kUnroll][2];
+        __half2 sl[kUnroll][2];
+        int64_t o[kUnroll];
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(page + x * ps * (D / 2) +
-                                                                   row * (D / 2) + wd * 4);
-            const __half2 sl = *(reinterpret_cast<const __half2 *>(page + ps * D + x * ps * kGroups * 4) +
-                                 row * kGroups + wd / 8);
-            const float step = __low2float(sl), low = __high2float(sl);
-            float f[8];
+        for (int i = 0; i < kUnroll; i++) {
+            o[i] = -1;
+            if (tl < tokens && s_w.base[tl] >= 0) {
+                const int row = s_w.pos[tl] & (ps - 1);
+                const uint8_t *page = p.s.cache + s_w.base[tl] + h * page_bytes;
+                o[i] = ((int64_t)(t0 + tl) * Hkv + h) * p.rep * D + wd * 8;
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                f[j] = __fadd_rn(__fmul_rn((float)((w >> (4 * j)) & 15u), step), low);
-            const uint4 u = store8<T>(f);
-            T *out = static_cast<T *>(x ? p.v_out : p.k_out) + o;
-            for (int r = 0; r < p.rep; r++)
-                *reinterpret_cast<uint4 *>(out + r * D) = u;
+                for (int x = 0; x < 2; x++) {
+                    w[i][x] = __ldg(reinterpret_cast<const uint32_t *>(page + (x * ps + row) * (D / 2)) + wd);
+                    sl[i][x] = __ldg(reinterpret_cast<const __half2 *>(page + ps * D + (x * ps + row) * (kGroups * 4)) +
+                                     wd / 8);
+                }
+            }
+            tl += dt;
+            h += dh;
+            if (h >= Hkv) {
+                h -= Hkv;
+                tl++;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; i++) {
+            if (o[i] < 0)
+                continue;
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const float step = __low2float(sl[i][x]), low = __high2float(sl[i][x]);
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++)            // the product is exact: 11 bits times 4
+                    f[j] = fmaf((float)((w[i][x] >> (4 * j)) & 15u), step, low);
+                const uint4 v = store8<T>(f);
+                T *out = static_cast<T *>(x ? p.v_out : p.k_out) + o[i];
+                for (int r = 0; r < p.rep; r++)
+                    *reinterpret_cast<uint4 *>(out + r * D) = v;
+            }
         }
     }
 }
 
 }  // namespace
 
+namespace {
+template <typename T, int D, int TOKENS>
+cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
+{
+    const int gx = (a.s.total + TOKENS - 1) / TOKENS;
+    // few tokens: their heads spread over more CTAs
+    const int gy = std::max(1, std::min({((a.q ? a.Hq : 0) + 15) / 16, (a.s.Hkv + 3) / 4, 296 / gx}));
+    kv4_append_kernel<T, D, TOKENS><<<dim3(gx, gy), kThreads, 0, st>>>(a, (a.Hq + gy - 1) / gy,
+                                                                      (a.s.Hkv + gy - 1) / gy);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
+{
+    // with many tokens, as many in a CTA as give its threads an angle each
+    if (a.s.total >= 4 * 148)
+        return a.d == 128 ? launch_append<T, 128, 4>(a, st) : launch_append<T, 64, 8>(a, st);
+    return a.d == 128 ? launch_append<T, 128, 1>(a, st) : launch_append<T, 64, 1>(a, st);
+}
+}  // namespace
+
 cudaError_t launch_kv4_append(const Kv4AppendArgs &a, cudaStream_t st)
 {
-    // as many tokens as fill the threads with angles, once there are enough CTAs
-    const int tpc = a.s.total >= 4 * 148 ? 4 : 1;
-    const int gx = (a.s.total + tpc - 1) / tpc;
-    const int q_ctas = a.q ? std::max(1, std::min((a.Hq + 31) / 32, 296 / gx)) : 0;
-    const int gy = q_ctas + (gx < 296 || q_ctas == 0 ? 1 : 0);   // few tokens: keys and values apart
-    const dim3 grid(gx, gy);
-    auto go = [&](auto kern) { kern<<<grid, kThreads, 0, st>>>(a, tpc, q_ctas); };
-    if (a.bf16)
-        a.d == 128 ? go(kv4_append_kernel<__nv_bfloat16, 128>) : go(kv4_append_kernel<__nv_bfloat16, 64>);
-    else
-        a.d == 128 ? go(kv4_append_kernel<__half, 128>) : go(kv4_append_kernel<__half, 64>);
-    return cudaGetLastError();
+    return a.bf16 ? launch_append<__nv_bfloat16>(a, st) : launch_append<__half>(a, st);
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, cudaStream_t st)

@@ -6,12 +6,14 @@
 // The angle, its sine and its cosine are 64-bit (p f_i reaches 10^6 and more, where a
 // 32-bit angle is wrong by 0.06 and more) and rounded once to 32 bits with the factor m;
 // the rotation itself is four 32-bit products and two sums, each rounded on its own (no
-// fused multiply-add), so that the codes the cache gets from it are defined bit for bit.
+// fused multiply-add, except by -1), so that the codes the cache gets from it are defined bit for bit.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+
+#include "sm100_ptx.cuh"
 
 namespace sage {
 
@@ -65,13 +67,41 @@ __device__ __forceinline__ uint4 store8<__nv_bfloat16>(const float (&f)[8])
 }
 
 // (cos, sin) of position * freq, times mscale, rounded once to fp32.
+//
+// The angle x = RN(position freq), |x| < 2^31, is reduced by the nearest multiple k of pi/2
+// (Cody and Waite's method: pi/2 in two pieces). x - k P1 is exact: it is a multiple of 2^-52
+// below 1. Sine and cosine of the rest, at most pi/4, are their Taylor sums to the 17th and 18th
+// power, whose next terms are below 2^-60: what is left are a few roundings of 2^-53.
 __device__ __forceinline__ float2 rope_cos_sin(int position, double freq, double mscale,
                                                bool inverse)
 {
-    double s, c;
-    sincos((double)position * freq, &s, &c);
-    const float sf = (float)(s * mscale);
-    return make_float2((float)(c * mscale), inverse ? -sf : sf);
+    const double x = (double)position * freq;
+    const double kd = rint(x * 0.6366197723675814);    // 2 / pi
+    const int k = (int)(long long)kd;
+    double r = fma(kd, -1.5707963267948966, x);        // pi / 2: its 53 leading bits, then the next
+    r = fma(kd, -6.123233995736766e-17, r);
+    const double z = r * r;
+    double s = 1.0 / 355687428096000.0, c = -1.0 / 6402373705728000.0;   // 1/17!, -1/18!
+    s = fma(s, z, -1.0 / 1307674368000.0);
+    c = fma(c, z, 1.0 / 20922789888000.0);
+    s = fma(s, z, 1.0 / 6227020800.0);
+    c = fma(c, z, -1.0 / 87178291200.0);
+    s = fma(s, z, -1.0 / 39916800.0);
+    c = fma(c, z, 1.0 / 479001600.0);
+    s = fma(s, z, 1.0 / 362880.0);
+    c = fma(c, z, -1.0 / 3628800.0);
+    s = fma(s, z, -1.0 / 5040.0);
+    c = fma(c, z, 1.0 / 40320.0);
+    s = fma(s, z, 1.0 / 120.0);
+    c = fma(c, z, -1.0 / 720.0);
+    s = fma(s, z, -1.0 / 6.0);
+    c = fma(c, z, 1.0 / 24.0);
+    c = fma(c, z, -0.5);
+    s = fma(s * z, r, r);
+    c = fma(c, z, 1.0);
+    const double sn = k & 1 ? c : s, cn = k & 1 ? s : c;     // quadrant
+    const float sf = (float)((k & 2 ? -sn : sn) * mscale);
+    return make_float2((float)(((k + 1) & 2 ? -cn : cn) * mscale), inverse ? -sf : sf);
 }
 
 // A head's d channels are worked on in units of 16: eight pairs of a rotated unit, or 16
@@ -90,27 +120,51 @@ __device__ __forceinline__ RopeUnit rope_unit(int u, int rot, bool interleaved)
     return RopeUnit{16 * u, 16 * u + 8, r};
 }
 
-// Rotates a unit's two chunks in place; cs: the (cos, sin) of its eight pairs.
-__device__ __forceinline__ void rope_rotate(float (&x)[8], float (&y)[8], const float2 *cs,
-                                            bool interleaved)
-{
-    if (interleaved) {
+// a - b on packed pairs: one exactly rounded subtraction each.
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+
+// Cosines and sines of a unit's eight pairs.
+struct RopeAngles {
+    float2 c[4], s[4];
+    __device__ void load(const float *cos, const float *sin)
+    {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float2 e = cs[i], f = cs[4 + i];
-            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, e.x), __fmul_rn(b, e.y));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, e.x), __fmul_rn(a, e.y));
-            y[2 * i] = __fsub_rn(__fmul_rn(c, f.x), __fmul_rn(d, f.y));
-            y[2 * i + 1] = __fadd_rn(__fmul_rn(d, f.x), __fmul_rn(c, f.y));
+            c[i] = reinterpret_cast<const float2 *>(cos)[i];
+            s[i] = reinterpret_cast<const float2 *>(sin)[i];
         }
-    } else {
+    }
+};
+
+// Rotates two pairs, (a.x, b.x) and (a.y, b.y): a <- a c - b s, b <- b c + a s.
+__device__ __forceinline__ void rope_pairs(float2 &a, float2 &b, float2 c, float2 s)
+{
+    const float2 x = sub2(mul2(a, c), mul2(b, s));
+    b = add2(mul2(b, c), mul2(a, s));
+    a = x;
+}
+
+// Rotates a unit's two chunks in place.
+__device__ __forceinline__ void rope_rotate(float (&x)[8], float (&y)[8], const RopeAngles &cs,
+                                            bool interleaved)
+{
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2 e = cs[i];
-            const float a = x[i], b = y[i];
-            x[i] = __fsub_rn(__fmul_rn(a, e.x), __fmul_rn(b, e.y));
-            y[i] = __fadd_rn(__fmul_rn(b, e.x), __fmul_rn(a, e.y));
+    for (int i = 0; i < 4; i++) {
+        if (interleaved) {                             // pairs side by side, the unit's 16 channels in a row
+            float *v = i < 2 ? x + 4 * i : y + 4 * (i - 2);
+            float2 a = make_float2(v[0], v[2]), b = make_float2(v[1], v[3]);
+            rope_pairs(a, b, cs.c[i], cs.s[i]);
+            v[0] = a.x;
+            v[1] = b.x;
+            v[2] = a.y;
+            v[3] = b.y;
+        } else {
+            float2 a = make_float2(x[2 * i], x[2 * i + 1]), b = make_float2(y[2 * i], y[2 * i + 1]);
+            rope_pairs(a, b, cs.c[i], cs.s[i]);
+            x[2 * i] = a.x;
+            x[2 * i + 1] = a.y;
+            y[2 * i] = b.x;
+            y[2 * i + 1] = b.y;
         }
     }
 }
