@@ -586,45 +586,37 @@ def attn_decode(q_i8, q_scale, k_i8, k_scale, v, causal: bool = False, sm_scale:
     return out
 
 
-# Rotary positions and the paged 4-bit cache. These wrappers take tensors as a model has them
-# (views of a fused projection included) and check shapes, types and devices, since a wrong one
-# would read or write elsewhere. A decode step makes these calls once per layer and its kernels
-# take a few microseconds, so a call's checks are one expression, and what to say about a wrong
-# argument is worked out only once one is wrong; the calls go straight to the library.
+# Rotary positions and the paged 4-bit cache. A decode step makes these calls once per layer and
+# their kernels take a few microseconds, so the checks of shapes, types and devices, the outputs'
+# allocation and the call itself are compiled (csrc/binding.cpp, built beside libsage.so): 4 to
+# 6 us a call against 13 to 15 in Python. A wrong tensor raises ValueError there.
 
 ROPE_SCALINGS = {"plain": SAGE_ROPE_PLAIN, "linear": SAGE_ROPE_LINEAR, "base": SAGE_ROPE_BASE,
                  "parts": SAGE_ROPE_PARTS}
-_PAGES = (16, 32, 64, 128, 256)
-_Strides2, _Strides8, _Strides12 = ctypes.c_int64 * 2, ctypes.c_int64 * 8, ctypes.c_int64 * 12
-_torch = None       # torch, its 16-bit types' codes, and what gives a device's current stream
-_half = {}
-_raw_stream = None
+_calls = None
 
 
-def _setup():
-    global _torch, _raw_stream
-    import torch
-    _half.update({torch.float16: SAGE_F16, torch.bfloat16: SAGE_BF16})
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _torch = torch
-    lib()
-    return torch
+def _bound():
+    """The compiled binding, bound to the library's entry points; raises if it is missing."""
+    global _calls
+    import torch  # noqa: F401  (its libraries first)
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        raise RuntimeError("quantized_attention_03_b200/_binding.so is missing or does not fit this torch: "
+                           "build it with `python -m quantized_attention_03_b200.build`") from e
+    L = lib()
+    b.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+        "sage_rope", "sage_kv4_append", "sage_kv4_gather", "sage_attn_kv4", "sage_attn_kv4_workspace_size")))
+    _calls = b
+    return b
 
 
-def _refuse(*wants):
-    """Raises for the first (tensor, what it has to be, whether it is) that is not."""
-    for x, what, ok in wants:
-        if not ok:
-            got = "None" if x is None else f"{str(x.dtype).replace('torch.', '')} {list(x.shape)} " \
-                f"with strides {list(x.stride())} on {x.device}"
-            raise ValueError(f"{what}, got {got}")
-    raise ValueError("the tensors' shapes, types and devices do not fit together")
-
-
-def _elsewhere(device: int) -> bool:
-    """Whether a device other than the tensors' (-1: the CPU's) is the current one."""
-    return device >= 0 and device != _torch.cuda.current_device()
+def _done(name: str, r):
+    """What a compiled call returned, or the error it stands for."""
+    if type(r) is int:
+        raise SageError(name, r)
+    return r
 
 
 def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -649,59 +641,9 @@ def rope(q, k, freqs, positions=None, mscale: float = 1.0, interleaved: bool = F
     strides; k may be None): (q_out, k_out). freqs and mscale: rope_freqs. positions int32 [N],
     [B, N] or [T]; None: 0 .. N-1. interleaved: pairs (2i, 2i+1), else (i, i + rot/2). inverse:
     the rotation back, which is also its gradient. q_out=q, k_out=k rotates in place."""
-    torch = _torch or _setup()
-    dims, dev, dtype = q.dim(), q.get_device(), q.dtype
-    if dims == 3:
-        (N, Hq, d), B = q.shape, 1
-    elif dims == 4:
-        B, Hq, N, d = q.shape
-    else:
-        _refuse((q, "q is [B, H, N, d] or [T, H, d]", False))
-    Hk = 0 if k is None else k.shape[1] if k.dim() == dims else -1
-    kshape = (N, Hk, d) if dims == 3 else (B, Hk, N, d)
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None and k is not None else k_out
-    qs, qos = q.stride(), q_out.stride()
-    ks, kos = (k.stride(), k_out.stride()) if k is not None else (qs, qs)
-    code = _half.get(dtype)
-    if not (code is not None and qs[-1] == 1 == qos[-1] and q_out.shape == q.shape
-            and q_out.dtype == dtype and q_out.get_device() == dev
-            and (k is None or (k.shape == kshape and k_out.shape == kshape and ks[-1] == 1 == kos[-1]
-                               and k.dtype == dtype and k_out.dtype == dtype and k.get_device() == dev
-                               and k_out.get_device() == dev))
-            and freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous()
-            and freqs.get_device() == dev
-            and (positions is None or (positions.dtype == torch.int32 and positions.get_device() == dev
-                                       and positions.shape in ((N,), (B, N))
-                                       and (N < 2 or positions.stride(-1) == 1)))):
-        _refuse((q, "q is float16 or bfloat16 [B, H, N, d] or [T, H, d], its channels contiguous",
-                 code is not None and qs[-1] == 1),
-                (q_out, "q_out has q's shape, type and device", q_out.shape == q.shape
-                 and q_out.dtype == dtype and q_out.device == q.device and qos[-1] == 1),
-                (k, "k has q's type, device, tokens and head dim", k is None or (
-                    k.shape == kshape and k.dtype == dtype and k.device == q.device and ks[-1] == 1)),
-                (k_out, "k_out has k's shape, type and device", k is None or (
-                    k_out.shape == kshape and k_out.dtype == dtype and k_out.device == q.device and kos[-1] == 1)),
-                (freqs, "freqs is a contiguous float64 vector on q's device", freqs.dtype == torch.float64
-                 and freqs.dim() == 1 and freqs.is_contiguous() and freqs.device == q.device),
-                (positions, "positions is int32 [N], [B, N] or [T] on q's device", False))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return rope(q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out, stream)
-    if dims == 3:
-        strides = _Strides12(0, qs[1], qs[0], 0, qos[1], qos[0], 0, ks[1], ks[0], 0, kos[1], kos[0])
-    else:
-        strides = _Strides12(*qs[:3], *qos[:3], *ks[:3], *kos[:3])
-    rc = _lib.sage_rope(
-        q.data_ptr(), q_out.data_ptr(), None if k is None else k.data_ptr(),
-        None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
-        freqs.data_ptr(), code, B, N, Hq, Hk, d, 2 * freqs.shape[0],
-        positions.stride(0) if positions is not None and positions.dim() == 2 else 0, strides, mscale,
-        (SAGE_ROPE_INTERLEAVED if interleaved else 0) | (SAGE_ROPE_INVERSE if inverse else 0),
-        _raw_stream(dev) if stream is None else _stream(stream))
-    if rc:
-        raise SageError("sage_rope", rc)
-    return q_out, k_out
+    return _done("sage_rope", (_calls or _bound()).rope(
+        q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out,
+        None if stream is None else _stream(stream)))
 
 
 def kv4_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):
@@ -713,33 +655,6 @@ def kv4_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):
     return torch.empty((num_pages, Hkv, n), dtype=torch.uint8, device=device)
 
 
-def _kv4(cache, block_table, kv_lens, cu_seqlens, d: int):
-    """Checked sizes of a cache and its sequences: (nseq, Hkv, page_size, num_pages, max_pages, device)."""
-    torch = _torch or _setup()
-    i32, dev = torch.int32, cache.get_device()
-    num_pages, Hkv, page_bytes = cache.shape if cache.dim() == 3 else (0, 0, 0)
-    page_size = page_bytes * 8 // (9 * d) if d > 0 else 0
-    nseq = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-    max_pages = block_table.shape[1] if block_table.dim() == 2 else -1
-    if not (page_size in _PAGES and page_size * 9 * d == page_bytes * 8 and cache.dtype == torch.uint8
-            and cache.is_contiguous() and nseq >= 0 and kv_lens.dtype == i32 and kv_lens.is_contiguous()
-            and kv_lens.get_device() == dev and block_table.shape == (nseq, max_pages)
-            and block_table.dtype == i32 and block_table.is_contiguous()
-            and block_table.get_device() == dev
-            and (cu_seqlens is None or (cu_seqlens.shape == (nseq + 1,) and cu_seqlens.dtype == i32
-                                        and cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev))):
-        fits = lambda x, shape: (x.dtype == i32 and x.is_contiguous() and x.device == cache.device  # noqa: E731
-                                 and tuple(x.shape) == shape)
-        _refuse((cache, "cache is a contiguous uint8 [num_pages, Hkv, page bytes] of kv4_cache for this head dim",
-                 page_size in _PAGES and page_size * 9 * d == page_bytes * 8
-                 and cache.dtype == torch.uint8 and cache.is_contiguous()),
-                (kv_lens, "kv_lens is contiguous int32 [nseq] on the cache's device", fits(kv_lens, (nseq,))),
-                (block_table, "block_table is contiguous int32 [nseq, max_pages] on the cache's device",
-                 fits(block_table, (nseq, max_pages))),
-                (cu_seqlens, "cu_seqlens is contiguous int32 [nseq + 1] on the cache's device", False))
-    return nseq, Hkv, page_size, num_pages, max_pages, dev
-
-
 def kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q=None, freqs=None,
                mscale: float = 1.0, interleaved: bool = False, k_mean=None, q_out=None,
                stream=None):
@@ -749,51 +664,9 @@ def kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q=None, freqs=None
     alike, or None. kv_lens int32 [nseq] counts the new tokens, cu_seqlens int32 [nseq+1] says
     which rows are whose (None: T / nseq each), block_table int32 [nseq, max_pages] where the
     pages are."""
-    torch = _torch or _setup()
-    T, Hkv, d = k.shape
-    nseq, heads, page_size, num_pages, max_pages, dev = _kv4(cache, block_table, kv_lens, cu_seqlens, d)
-    dtype, shape = k.dtype, k.shape
-    code = _half.get(dtype)
-    ks, vs = k.stride(), v.stride()
-    Hq, qs, qos, qp, qop = 0, ks, ks, None, None
-    q_ok = True
-    if q is not None:
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        qs, qos, Hq = q.stride(), q_out.stride(), q.shape[1]
-        q_ok = (q.shape == (T, Hq, d) and q_out.shape == q.shape and q.dtype == dtype
-                and q_out.dtype == dtype and qs[2] == 1 == qos[2] and q.get_device() == dev
-                and q_out.get_device() == dev)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    if not (code is not None and heads == Hkv and v.shape == shape and v.dtype == dtype and q_ok
-            and ks[2] == 1 == vs[2] and k.get_device() == dev and v.get_device() == dev
-            and (freqs is None or (freqs.dtype == torch.float64 and freqs.dim() == 1
-                                   and freqs.is_contiguous() and freqs.get_device() == dev))
-            and (k_mean is None or (k_mean.dtype == torch.float32 and k_mean.shape == (Hkv, d)
-                                    and k_mean.is_contiguous() and k_mean.get_device() == dev))):
-        _refuse((k, "k is float16 or bfloat16 [T, Hkv, d] with the cache's heads and device, its channels contiguous",
-                 code is not None and heads == Hkv and ks[2] == 1 and k.device == cache.device),
-                (v, "v has k's shape, type and device", v.shape == shape and v.dtype == dtype
-                 and vs[2] == 1 and v.device == cache.device),
-                (q, "q is [T, Hq, d] of k's type and device, and q_out like it", q_ok),
-                (freqs, "freqs is a contiguous float64 vector on the cache's device", freqs is None or (
-                    freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous()
-                    and freqs.device == cache.device)),
-                (k_mean, "k_mean is a contiguous float32 [Hkv, d] on the cache's device", False))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q, freqs, mscale,
-                              interleaved, k_mean, q_out, stream)
-    rc = _lib.sage_kv4_append(
-        cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-        None if cu_seqlens is None else cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), qp, qop,
-        None if freqs is None else freqs.data_ptr(), None if k_mean is None else k_mean.data_ptr(), code,
-        nseq, T, Hq, Hkv, d, page_size, num_pages, max_pages, 0 if freqs is None else 2 * freqs.shape[0],
-        _Strides8(ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], qos[0], qos[1]), mscale,
-        SAGE_ROPE_INTERLEAVED if interleaved else 0,
-        _raw_stream(dev) if stream is None else _stream(stream))
-    if rc:
-        raise SageError("sage_kv4_append", rc)
-    return q_out
+    return _done("sage_kv4_append", (_calls or _bound()).kv4_append(
+        cache, block_table, kv_lens, cu_seqlens, k, v, q, freqs, mscale, interleaved, k_mean, q_out,
+        None if stream is None else _stream(stream)))
 
 
 def kv4_gather(cache, block_table, kv_lens, cu_seqlens, total: int, d: int, dtype=None,
@@ -801,31 +674,12 @@ def kv4_gather(cache, block_table, kv_lens, cu_seqlens, total: int, d: int, dtyp
     """The last cu_seqlens[s+1] - cu_seqlens[s] tokens of every sequence as 16-bit k and v
     [total, Hkv * rep, d], each head rep times (dtype float16 by default): what
     sageattn_varlen_kv takes for a prefill chunk over cached keys."""
-    torch = _torch or _setup()
-    nseq, Hkv, page_size, num_pages, max_pages, dev = _kv4(cache, block_table, kv_lens, cu_seqlens, d)
-    dtype = torch.float16 if dtype is None else dtype
-    shape = (total, Hkv * rep, d)
-    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-    v_out = torch.empty_like(k_out) if v_out is None else v_out
-    code = _half.get(dtype)
-    if not (code is not None and k_out.shape == shape and v_out.shape == shape and k_out.dtype == dtype
-            and v_out.dtype == dtype and k_out.is_contiguous() and v_out.is_contiguous()
-            and k_out.get_device() == dev and v_out.get_device() == dev):
-        fits = lambda x: (code is not None and x.shape == shape and x.dtype == dtype and x.is_contiguous()  # noqa: E731
-                          and x.device == cache.device)
-        what = f"contiguous {dtype} {list(shape)} on the cache's device, float16 or bfloat16"
-        _refuse((k_out, f"k_out is {what}", fits(k_out)), (v_out, f"v_out is {what}", fits(v_out)))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return kv4_gather(cache, block_table, kv_lens, cu_seqlens, total, d, dtype, rep, k_out, v_out, stream)
-    rc = _lib.sage_kv4_gather(
-        cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-        None if cu_seqlens is None else cu_seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), code,
-        nseq, total, Hkv, rep, d, page_size, num_pages, max_pages,
-        _raw_stream(dev) if stream is None else _stream(stream))
-    if rc:
-        raise SageError("sage_kv4_gather", rc)
-    return k_out, v_out
+    import torch
+    if dtype not in (None, torch.float16, torch.bfloat16):
+        raise ValueError(f"dtype is float16 or bfloat16, got {dtype}")
+    return _done("sage_kv4_gather", (_calls or _bound()).kv4_gather(
+        cache, block_table, kv_lens, cu_seqlens, total, d, dtype is torch.bfloat16, rep, k_out, v_out,
+        None if stream is None else _stream(stream)))
 
 
 def attn_kv4(q, cache, block_table, kv_lens, cu_seqlens=None, max_q: Optional[int] = None,
@@ -835,43 +689,9 @@ def attn_kv4(q, cache, block_table, kv_lens, cu_seqlens=None, max_q: Optional[in
     head h reads key head h // (Hq / Hkv). A sequence has at most max_q queries (by default T /
     nseq without cu_seqlens, else DECODE_MAX_Q), which are its last tokens. lse: float32 [T, Hq]
     that takes the log of the softmax sums. The workspace is allocated here unless given."""
-    torch = _torch or _setup()
-    T, Hq, d = shape = q.shape
-    nseq, Hkv, page_size, num_pages, max_pages, dev = _kv4(cache, block_table, kv_lens, cu_seqlens, d)
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
-    dtype, qs = q.dtype, q.stride()
-    code = _half.get(dtype)
-    if not (code is not None and qs[2] == 1 and q.get_device() == dev and out.shape == shape
-            and out.dtype == dtype and out.is_contiguous() and out.get_device() == dev
-            and (lse is None or (lse.dtype == torch.float32 and lse.shape == (T, Hq)
-                                 and lse.is_contiguous() and lse.get_device() == dev))
-            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
-        _refuse((q, "q is float16 or bfloat16 [T, Hq, d] on the cache's device, its channels contiguous",
-                 code is not None and qs[2] == 1 and q.device == cache.device),
-                (out, "out is contiguous and has q's shape, type and device", out.shape == shape
-                 and out.dtype == dtype and out.is_contiguous() and out.device == q.device),
-                (lse, "lse is a contiguous float32 [T, Hq] on q's device", lse is None or (
-                    lse.dtype == torch.float32 and lse.shape == (T, Hq) and lse.is_contiguous()
-                    and lse.device == q.device)),
-                (workspace, "workspace is contiguous and on q's device", False))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return attn_kv4(q, cache, block_table, kv_lens, cu_seqlens, max_q, causal, sm_scale, out, lse,
-                            workspace, stream)
-    if max_q is None:
-        max_q = DECODE_MAX_Q if cu_seqlens is not None else T // max(nseq, 1)
-    if workspace is None:
-        workspace = torch.empty(max(_lib.sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d), 16),
-                                dtype=torch.uint8, device=cache.device)
-    rc = _lib.sage_attn_kv4(
-        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-        None if cu_seqlens is None else cu_seqlens.data_ptr(), out.data_ptr(),
-        None if lse is None else lse.data_ptr(), code, nseq, T, max_q, Hq, Hkv, d, page_size, num_pages,
-        max_pages, 1 if causal else 0, sm_scale, _Strides2(qs[0], qs[1]), workspace.data_ptr(),
-        workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream))
-    if rc:
-        raise SageError("sage_attn_kv4", rc)
-    return out
+    return _done("sage_attn_kv4", (_calls or _bound()).attn_kv4(
+        q, cache, block_table, kv_lens, cu_seqlens, max_q, causal, sm_scale, out, lse, workspace,
+        None if stream is None else _stream(stream)))
 
 
 def qk_int32(q_i8, k_i8, stream=None):

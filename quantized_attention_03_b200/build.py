@@ -9,6 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsage.so")
+BINDING = os.path.join(HERE, "_binding.so")     # tensors to C ABI calls (csrc/binding.cpp)
 SOURCES = ["api.cu", "kv4_api.cu", "quant.cu", "attn_sm100.cu", "decode.cu", "rope.cu", "kv4.cu",
            "kv4_attn.cu", "selftest.cu"]
 HEADERS = ["sage_common.cuh", "sm100_ptx.cuh", "quant_codes.cuh", "decode.cuh", "rope.cuh",
@@ -27,6 +28,37 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def _binding_stale() -> bool:
+    deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "sage.h")]
+    return not os.path.exists(BINDING) or any(
+        os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps)
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the Python extension that makes the rotary and 4-bit cache calls (g++, torch's
+    headers and libraries)."""
+    if not force and not _binding_stale():
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [os.path.join(base, "include"), os.path.join(base, "include/torch/csrc/api/include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(base, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(x for p in include for x in ("-isystem", p)), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + r.stdout.decode(errors="replace"))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -37,7 +69,9 @@ def _stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source into one shared library (objects built in parallel)."""
+    """Compile every CUDA source into one shared library (objects built in parallel), and the
+    Python extension beside it."""
+    build_binding(force)
     if not force and not _stale():
         return LIB
     objdir = os.path.join(ROOT, "_build")

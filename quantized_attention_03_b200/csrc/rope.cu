@@ -4,8 +4,8 @@
 // One CTA takes a few neighbouring tokens with their heads, so that a token's 64-bit sines and
 // cosines (one per pair, 64 at d = 128) are computed once. A thread keeps one place, 16 channels
 // of one token (both halves of eight pairs, so a rotation in place is safe), holds their sines
-// and cosines in registers and walks over the heads, two at a time with all loads in flight. (Four at a time cost the registers
-// of two more CTAs an SM: 95 against 87 us for 537 MB.)
+// and cosines in registers and walks over the heads, two at a time with all loads in flight.
+// (Four at a time cost the registers of two more CTAs an SM: 95 against 87 us for 537 MB.)
 #include <algorithm>
 
 #include "rope.cuh"
