@@ -9,13 +9,14 @@
 //
 // What bounds it: the cache is read once from HBM, 0.5625 bytes per element, and each
 // element has to be turned from 4 bits into a 16-bit operand, so the instructions that
-// unpack (0.6 per key element, 1.3 per value element) are the second bound.
-//   - Keys: a code masked in place is an fp16 subnormal, n 2^-24 or 16 n 2^-24, which the
-//     tensor core multiplies exactly; one AND makes two operands. The queries of the second
-//     kind of channel are divided by 16 beforehand.
-//   - Values: codes are centred (n - 8), two operands per OR/AND and packed add, because the
-//     sum of p n' stays near the size of its result; uncentred it would be the difference of
-//     two sums 100 times larger, in which the accumulator's own rounding shows.
+// unpack (0.6 per key element, 0.9 per value element) are the second bound.
+//   - A code masked in place is an fp16 subnormal, n 2^-24 or 16 n 2^-24, which the tensor core
+//     multiplies exactly; one AND makes two operands. The queries of the second kind of channel
+//     are divided by 16 beforehand, the outputs' at the end.
+//   - Values are centred (n - 8), because the sum of p n' stays near the size of its result;
+//     uncentred it would be the difference of two sums 100 times larger over a long cache, in
+//     which the accumulator's own rounding shows. One product with constant codes -8 gives what
+//     a tile has to be lessened by, the same for all channels.
 //   - Probabilities times step are split into two fp16 terms, high and low, each with its own
 //     product: one term alone would round every p to 11 bits, as much error again as the
 //     rounding of the 16-bit output.
@@ -33,6 +34,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "rope.cuh"
@@ -41,20 +43,15 @@
 namespace sage {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kMergeWarps = 8;
 constexpr int kSMs = 148;
 // Places that the start of a segment takes in the list of work, in tiles: what it costs a CTA
 // to start on one (queries, pages, first tile, merge), or a warp that works alone.
-#ifndef SOLOC
-#define SOLOC 2
-#endif
-#ifndef SOLOS
-#define SOLOS 148
-#endif
-constexpr int kTeamCost = 16, kSoloCost = SOLOC;
+constexpr int kTeamCost = 16, kSoloCost = 2;
 // From so many segments on, every warp works alone on its own share; below, a CTA's warps share one.
-constexpr int kSoloSegments = SOLOS;
+constexpr int kSoloSegments = kSMs;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -65,8 +62,8 @@ template <int D, int NT, bool FOLD>
 struct Cfg {
     static constexpr int kTile = 4096 / D;             // keys per warp tile
     static constexpr int kGroups = D / kKv4Group;
-    static constexpr int kStages = NT == 1 ? 2 : 4;
-    static constexpr int kCtasPerSM = NT == 1 ? 2 : 1;
+    static constexpr int kStages = NT == 1 ? 2 : 3;
+    static constexpr int kCtasPerSM = NT == 1 ? 3 : 2;   // 168 or 255 registers a thread
     static constexpr int kRows = FOLD ? 4 : 8 * NT;
     static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
     static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
@@ -99,6 +96,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with no sum to add to.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // 8x8 transpose of 16-bit elements over the warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
@@ -115,14 +122,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// (x & mask) | 0x6400 in both halves: the fp16 number 1024 + code (or 1024 + 16 code).
-template <uint32_t kMask>
-__device__ __forceinline__ uint32_t biased(uint32_t x)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "n"(kMask), "r"(0x64006400u));
-    return r;
-}
+// -8 and -128 times 2^-24, twice: what centres the codes of the two kinds of channel.
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
 
 // (step, low) of a key's or value's groups.
 template <int G>
@@ -442,7 +443,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 atomicOr(sq.status, status_bit(SAGE_ERR_BAD_PAGE));
                 ids = 0;
             }
-            __syncwarp();
             if (left >= C::kTile && slice == C::kTile) {       // a whole tile of one page
                 const int row = k0 & (ps - 1);
                 const uint8_t *src = head + __shfl_sync(0xffffffffu, ids, 0) * page_stride;
@@ -473,7 +473,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        stage_in = stage_in + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : stage_in + C::kStageBytes;
+        stage_in = C::kStages == 2                                     ? stage_in ^ C::kStageBytes
+                   : stage_in == (C::kStages - 1) * C::kStageBytes ? 0
+                                                                   : stage_in + C::kStageBytes;
         next_tile += step;
         if (more)
             advance();
@@ -554,14 +556,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             }
         }
         const float2 low_sel = t4 < 2 ? make_float2(0.0f, 0.0f) : make_float2(-1.0f, -1.0f);
-        int vexp = -64;                                // exponent the value products are scaled for
+        // exponent the value products are scaled for; steps from vlimit on (as fp16 bits) are too
+        // large for it
+        int vexp = -64;
+        uint32_t vlimit = 0;
+        float vscale = 1.0f;
 
         for (int t = seg.t0 + place; t < end; t += step) {
             const int k0 = t * C::kTile;
             const uint8_t *st = ring + stage_out;
             asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
             __syncwarp();                              // every lane's part has landed
-            const bool masked = k0 + C::kTile - 1 > seen;
+            auto tile = [&](auto hides) {
+            constexpr bool masked = decltype(hides)::value;
 
             // ---- scores, S^T: rows are keys, columns query rows; s f is the base-2 logit
             float s[kKB][NT][4];
@@ -577,16 +584,20 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 for (int gr = 0; gr < kG; gr++) {
                     const uint2 w0 = *reinterpret_cast<const uint2 *>(r0p + gr * 32);
                     const uint2 w1 = *reinterpret_cast<const uint2 *>(r1p + gr * 32);
-                    float acc[NT][4] = {};
+                    float acc[NT][4];
 #pragma unroll
                     for (int j = 0; j < 2; j++) {
                         uint32_t u0 = j ? w0.y : w0.x, u1 = j ? w1.y : w1.x;
 #pragma unroll
                         for (int hf = 0; hf < 2; hf++) {
+                            const uint32_t a0 = u0 & 0x000F000Fu, a1 = u1 & 0x000F000Fu;
+                            const uint32_t a2 = u0 & 0x00F000F0u, a3 = u1 & 0x00F000F0u;
 #pragma unroll
                             for (int i = 0; i < NT; i++)
-                                mma16816(acc[i], u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u,
-                                         u1 & 0x00F000F0u, qf[i][gr][j][2 * hf], qf[i][gr][j][2 * hf + 1]);
+                                if (j == 0 && hf == 0)
+                                    mma16816_first(acc[i], a0, a1, a2, a3, qf[i][gr][0][0], qf[i][gr][0][1]);
+                                else
+                                    mma16816(acc[i], a0, a1, a2, a3, qf[i][gr][j][2 * hf], qf[i][gr][j][2 * hf + 1]);
                             u0 >>= 8;
                             u1 >>= 8;
                         }
@@ -617,7 +628,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
 
             // ---- the reference m that probabilities are taken relative to moves only when a
             // logit is more than 8 above it, so p <= 2^8
-            float alpha[NT][2];
             float x[NT][2];
             bool move = false;
 #pragma unroll
@@ -628,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
 #pragma unroll
                     for (int kb = 1; kb < kKB; kb++)
                         x[i][c] = fmaxf(x[i][c], fmaxf(s[kb][i][c], s[kb][i][c + 2]));
-                    alpha[i][c] = 1.0f;
                     move |= fmaf(x[i][c], f[i][c], nm[i][c]) > 8.0f;
                 }
             // ---- the tile's largest value step: products p * step are scaled by a power of two
@@ -644,42 +653,43 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= len)
                     vs.y = 0;
             }
-            const int texp = (int)(__reduce_max_sync(0xffffffffu, max(vs.x, vs.y)) >> 10);
-            float shift = 1.0f;
-            if (texp > vexp + 3) {
-                shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
-                vexp = texp;
-                move = true;
-            }
-            if (__any_sync(0xffffffffu, move)) {
+            const uint32_t vtop = max(vs.x, vs.y);
+            if (__any_sync(0xffffffffu, move || vtop >= vlimit)) {
+                const int texp = (int)(__reduce_max_sync(0xffffffffu, vtop) >> 10);
+                float shift = 1.0f;
+                if (texp > vexp + 3) {
+                    shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
+                    vexp = texp;
+                    vlimit = (uint32_t)(vexp + 4) << 10;
+                    vscale = __uint_as_float((uint32_t)(127 + 18 - vexp) << 23);
+                }
 #pragma unroll
                 for (int i = 0; i < NT; i++)
 #pragma unroll
                     for (int c = 0; c < 2; c++) {
-                        float y = x[i][c];
+                        float y = x[i][c], alpha = 1.0f;
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) * f[i][c];
                         if (y > -nm[i][c]) {           // (rows that have seen no key: -inf on both sides)
-                            alpha[i][c] = ex2_approx(-nm[i][c] - y);
+                            alpha = ex2_approx(-nm[i][c] - y);
                             nm[i][c] = -y;
                         }
-                        l[i][c] *= alpha[i][c];
-                        const float as = alpha[i][c] * shift;
+                        l[i][c] *= alpha;
 #pragma unroll
                         for (int gr = 0; gr < kG; gr++) {
-                            o2[i][gr][c] *= alpha[i][c];
+                            o2[i][gr][c] *= alpha;
 #pragma unroll
                             for (int j = 0; j < 4; j++) {
-                                o[i][gr][j][c] *= as;
-                                o[i][gr][j][c + 2] *= as;
+                                o[i][gr][j][c] *= alpha * shift;
+                                o[i][gr][j][c + 2] *= alpha * shift;
                             }
                         }
                     }
             }
-            const float vscale = __uint_as_float((uint32_t)(127 + 18 - vexp) << 23);
 
             // ---- probabilities and O^T += V^T P^T: rows are channels, columns query rows
+            float centre[NT][kG][4];
 #pragma unroll
             for (int kb = 0; kb < kKB; kb++) {
 #pragma unroll
@@ -743,19 +753,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                     const uint32_t wb = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + D / 2);
                     const uint32_t wc = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 8 * (D / 2));
                     const uint32_t wd = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 9 * (D / 2));
-                    const __half2 sub = bits_h2(0xE408E408u);         // -1032
-                    const __half2 sixteenth = bits_h2(0x2C002C00u);   // 1 / 16
-                    const __half2 sub16 = bits_h2(0xD480D480u);       // -72
+                    // minus 8 (and 128) for every code of the block, into sums of their own
+#pragma unroll
+                    for (int i = 0; i < NT; i++) {
+                        if (kb == 0)
+                            mma16816_first(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, hi[i][0], hi[i][1]);
+                        else
+                            mma16816(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, hi[i][0], hi[i][1]);
+                        if (!FOLD)
+                            mma16816(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, lo[i][0], lo[i][1]);
+                    }
 #pragma unroll
                     for (int q = 0; q < 2; q++) {      // channels 0-3, then 4-7 of the word
                         uint32_t ab = __byte_perm(wa, wb, q ? 0x7632 : 0x5410);
                         uint32_t cd = __byte_perm(wc, wd, q ? 0x7632 : 0x5410);
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
-                            const uint32_t a0 = h2_bits(__hadd2(bits_h2(biased<0x000F000Fu>(ab)), sub));
-                            const uint32_t a1 = h2_bits(__hfma2(bits_h2(biased<0x00F000F0u>(ab)), sixteenth, sub16));
-                            const uint32_t a2 = h2_bits(__hadd2(bits_h2(biased<0x000F000Fu>(cd)), sub));
-                            const uint32_t a3 = h2_bits(__hfma2(bits_h2(biased<0x00F000F0u>(cd)), sixteenth, sub16));
+                            const uint32_t a0 = ab & 0x000F000Fu, a1 = ab & 0x00F000F0u;
+                            const uint32_t a2 = cd & 0x000F000Fu, a3 = cd & 0x00F000F0u;
 #pragma unroll
                             for (int i = 0; i < NT; i++) {
                                 mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, hi[i][0], hi[i][1]);
@@ -768,8 +783,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                     }
                 }
             }
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+#pragma unroll
+                for (int gr = 0; gr < kG; gr++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int c = 0; c < 4; c += 2) {
+                            const float2 y = add2(make_float2(o[i][gr][j][c], o[i][gr][j][c + 1]),
+                                                  make_float2(centre[i][gr][c], centre[i][gr][c + 1]));
+                            o[i][gr][j][c] = y.x;
+                            o[i][gr][j][c + 1] = y.y;
+                        }
+            };
+            if (k0 + C::kTile - 1 > seen)
+                tile(std::true_type{});
+            else
+                tile(std::false_type{});
             __syncwarp();                              // the stage is read
-            stage_out = stage_out + C::kStageBytes == C::kStages * C::kStageBytes ? 0 : stage_out + C::kStageBytes;
+            stage_out = C::kStages == 2                                      ? stage_out ^ C::kStageBytes
+                        : stage_out == (C::kStages - 1) * C::kStageBytes ? 0
+                                                                         : stage_out + C::kStageBytes;
             issue();
         }
 
@@ -780,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             const int64_t last = seg.x + cost + seg.nt;
             tail = Tail{(int)((last * teams + total - 1) / total) - 1, seg.row0, seg.n, seg.kvh, seg.rb};
         }
-        const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 - 18 + vexp) << 23);
+        const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + 6 + vexp) << 23);
         float *const part = p.part + (int64_t)(team * 2 + (seg.t0 == 0)) * (C::kRows * C::kPitch);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
@@ -809,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                             float y = o[i][gr][j][c + 2 * e];
                             if (FOLD)
                                 y += __shfl_xor_sync(0xffffffffu, y, 2);
-                            v[gr][2 * j + e] = fmaf(y, unscale, ow[gr]);
+                            v[gr][2 * j + e] = fmaf(y, e ? unscale * 0.0625f : unscale, ow[gr]);
                         }
                 if (r >= nrows || (FOLD && t4 >= 2))
                     continue;
@@ -897,12 +932,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
 // finish. Its warps take the rows, several a row where the rows are few, eight partials at a
 // time (all their loads in flight together), always in the same order.
 template <int D, int NT, bool FOLD>
-__global__ void __launch_bounds__(kThreads) kv4_attn_merge(const Params p)
+__global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params p)
 {
     using C = Cfg<D, NT, FOLD>;
     constexpr int kC = D / 32, kChunk = 8;             // channels of a lane, partials at a time
-    __shared__ __align__(16) float s_part[kWarps][D];
-    __shared__ float2 s_ml[kWarps];
+    __shared__ __align__(16) float s_part[kMergeWarps][D];
+    __shared__ float2 s_ml[kMergeWarps];
     griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, team = blockIdx.x;
     if (*p.solo == 0 && team >= gridDim.x / kWarps)
@@ -914,7 +949,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_merge(const Params p)
     const int split = nrows <= 1 ? 8 : nrows <= 2 ? 4 : nrows <= 4 ? 2 : 1;   // warps of a row
     const int each = (t.last - team + split) / split, part = warp % split;
     const int c0 = team + part * each, c1 = min(t.last + 1, c0 + each);
-    for (int base = 0; base < nrows; base += kWarps / split) {
+    for (int base = 0; base < nrows; base += kMergeWarps / split) {
         const int r = base + warp / split;
         float M = -INFINITY, L = 0.0f, acc[kC] = {};
         for (int c = c0; r < nrows && c < c1; c += kChunk) {
@@ -984,7 +1019,7 @@ int variant(int Hq, int Hkv, int max_q)
     const int rows = max_q * (Hq / Hkv);
     return rows <= 4 ? 0 : rows <= 8 ? 1 : 2;
 }
-int ctas(int var) { return var < 2 ? 2 * kSMs : kSMs; }
+int ctas(int var) { return (var < 2 ? 3 : 2) * kSMs; }
 int rows_of(int var) { return 4 << var; }
 
 template <int D, int NT, bool FOLD>
@@ -1004,7 +1039,7 @@ cudaError_t launch(const Params &p, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n * kWarps);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
