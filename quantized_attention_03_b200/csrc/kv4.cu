@@ -18,23 +18,36 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;    // tokens one CTA takes at most
 
-// Last sequence whose first row is at or before row t (cu non-decreasing), found by a whole
-// warp: each round looks at 32 spread places at once, so 1024 sequences take two rounds.
-__device__ int find_sequence(const Kv4Seqs &s, int t)
+// The last sequence whose first row is at or before row t (cu non-decreasing), its rows a .. b-1
+// and its length, found by a whole warp: each round looks at 32 spread places at once, and the
+// last loads what goes with them, so up to 32 sequences take one round trip and 1024 two.
+__device__ int find_sequence(const Kv4Seqs &s, int t, int &a, int &b, int &len)
 {
-    if (s.cu == nullptr)
-        return min(t / (s.total / s.nseq), s.nseq - 1);
+    if (s.cu == nullptr) {
+        const int n = s.total / s.nseq, seq = min(t / n, s.nseq - 1);
+        a = seq * n;
+        b = a + n;
+        len = __ldg(s.kv_lens + seq);
+        return seq;
+    }
     const int lane = threadIdx.x % 32;
     int lo = 0, n = s.nseq;                            // the answer is in [lo, lo + n)
-    while (n > 1) {
+    while (n > 32) {
         const int step = (n + 31) / 32;
-        const int i = lo + lane * step;
-        const bool le = lane * step < n && __ldg(s.cu + i) <= t;
+        const bool le = lane * step < n && __ldg(s.cu + lo + lane * step) <= t;
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
         lo += last * step;
         n = min(step, n - last * step);
     }
-    return lo;
+    const int i = lo + min(lane, n - 1);
+    a = __ldg(s.cu + i);
+    b = __ldg(s.cu + i + 1);
+    len = __ldg(s.kv_lens + i);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, lane < n && a <= t) | 1u);
+    a = __shfl_sync(0xffffffffu, a, last);
+    b = __shfl_sync(0xffffffffu, b, last);
+    len = __shfl_sync(0xffffffffu, len, last);
+    return lo + last;
 }
 
 // Where the CTA's tokens live: row t0 + i is token pos[i] of a sequence, in row slot of the
@@ -55,11 +68,11 @@ __device__ void find_places(const Kv4Seqs &s, int t0, int tokens, int64_t page_b
     }
     const int warp = threadIdx.x / 32;
     for (int i = warp; i < tokens; i += kThreads / 32) {
-        const int t = t0 + i, seq = find_sequence(s, t);
         int a, b, len, pos = -1;
+        const int t = t0 + i, seq = find_sequence(s, t, a, b, len);
         int64_t base = -1;
         // rows past the last sequence belong to nobody and are left alone
-        if (s.rows(seq, a, b, len) && t >= a && t < b) {
+        if (s.sound(a, b, len) && t >= a && t < b) {
             pos = len - (b - t);
             if (pos < 0) {
                 atomicOr(s.status, status_bit(SAGE_ERR_BAD_SEQLENS));
@@ -159,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, TOKENS == 1 ? 2 : 3) kv4_append_kern
     // cosines and sines, [TOKENS][rot / 2]
     __shared__ __align__(16) float s_c[TOKENS * D / 2], s_s[TOKENS * D / 2];
     __shared__ Places s_w;
+    griddep_launch_dependents();
     griddep_wait();
     const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, p.s.total - t0);
     const int64_t page_bytes = kv4_page_bytes(p.s.page_size(), D);
@@ -308,6 +322,7 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4GatherArg
 {
     constexpr int kWords = D / 8, kGroups = D / kKv4Group, kStep = kThreads / kWords, kUnroll = 2;
     __shared__ Places s_w;
+    griddep_launch_dependents();
     griddep_wait();
     const int t0 = blockIdx.x * tokens_per_cta;
     const int tokens = min(tokens_per_cta, p.s.total - t0);
@@ -372,9 +387,8 @@ cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
     const int gx = (a.s.total + TOKENS - 1) / TOKENS;
     // few tokens: their heads spread over more CTAs
     const int gy = std::max(1, std::min({((a.q ? a.Hq : 0) + 15) / 16, (a.s.Hkv + 3) / 4, 296 / gx}));
-    kv4_append_kernel<T, D, TOKENS><<<dim3(gx, gy), kThreads, 0, st>>>(a, (a.Hq + gy - 1) / gy,
-                                                                      (a.s.Hkv + gy - 1) / gy);
-    return cudaGetLastError();
+    return launch_overlapped(kv4_append_kernel<T, D, TOKENS>, dim3(gx, gy), kThreads, 0, st, a, (a.Hq + gy - 1) / gy,
+                             (a.s.Hkv + gy - 1) / gy);
 }
 template <typename T>
 cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
@@ -395,12 +409,10 @@ cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, cudaStream_t st)
 {
     const int tpc = a.s.total >= 8 * 4 * 148 ? 8 : 1;
     const int grid = (a.s.total + tpc - 1) / tpc;
-    auto go = [&](auto kern) { kern<<<grid, kThreads, 0, st>>>(a, tpc); };
+    auto go = [&](auto kern) { return launch_overlapped(kern, dim3(grid), kThreads, 0, st, a, tpc); };
     if (a.bf16)
-        a.d == 128 ? go(kv4_gather_kernel<__nv_bfloat16, 128>) : go(kv4_gather_kernel<__nv_bfloat16, 64>);
-    else
-        a.d == 128 ? go(kv4_gather_kernel<__half, 128>) : go(kv4_gather_kernel<__half, 64>);
-    return cudaGetLastError();
+        return a.d == 128 ? go(kv4_gather_kernel<__nv_bfloat16, 128>) : go(kv4_gather_kernel<__nv_bfloat16, 64>);
+    return a.d == 128 ? go(kv4_gather_kernel<__half, 128>) : go(kv4_gather_kernel<__half, 64>);
 }
 
 }  // namespace sage

@@ -54,13 +54,17 @@ struct Kv4Seqs {
             b = a + n;
         }
         len = __ldg(kv_lens + s);
-        if (a < 0 || b < a || b > total || len < 0 ||
-            (int64_t)len > ((int64_t)max_pages << page_log2)) {
-            atomicOr(status, status_bit(SAGE_ERR_BAD_SEQLENS));
-            a = b = len = 0;
-            return false;
-        }
-        return true;
+        if (sound(a, b, len))
+            return true;
+        a = b = len = 0;
+        return false;
+    }
+    __device__ bool sound(int a, int b, int len) const
+    {
+        if (a >= 0 && b >= a && b <= total && len >= 0 && (int64_t)len <= ((int64_t)max_pages << page_log2))
+            return true;
+        atomicOr(status, status_bit(SAGE_ERR_BAD_SEQLENS));
+        return false;
     }
     // Page of token j of sequence s, or -1 (and a status bit) if the table's entry is not one.
     __device__ int page(int s, int j) const

@@ -938,6 +938,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params 
     constexpr int kC = D / 32, kChunk = 8;             // channels of a lane, partials at a time
     __shared__ __align__(16) float s_part[kMergeWarps][D];
     __shared__ float2 s_ml[kMergeWarps];
+    griddep_launch_dependents();
     griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, team = blockIdx.x;
     if (*p.solo == 0 && team >= gridDim.x / kWarps)
@@ -1031,19 +1032,10 @@ cudaError_t launch(const Params &p, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     const int n = C::kCtasPerSM * kSMs;
-    kv4_attn_kernel<D, NT, FOLD><<<n, kThreads, C::kSmem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    e = launch_overlapped(kv4_attn_kernel<D, NT, FOLD>, dim3(n), kThreads, C::kSmem, st, p);
+    if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n * kWarps);
-    cfg.blockDim = dim3(kMergeWarps * 32);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_attn_merge<D, NT, FOLD>, p);
+    return launch_overlapped(kv4_attn_merge<D, NT, FOLD>, dim3(n * kWarps), kMergeWarps * 32, 0, st, p);
 }
 
 // [whether solo | tails], then the partial rows, of as many teams as there are warps

@@ -23,6 +23,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs p, int
     constexpr int kUnits = D / 16, kStep = kThreads / (TOKENS * kUnits), kUnroll = 2;
     // cosines and sines, [TOKENS][rot / 2]
     __shared__ __align__(16) float s_c[TOKENS * D / 2], s_s[TOKENS * D / 2];
+    griddep_launch_dependents();
     griddep_wait();
     const int half = p.rot / 2, all = p.B * p.N, t0 = blockIdx.x * TOKENS;
     for (int i = threadIdx.x; i < TOKENS * half; i += kThreads) {
@@ -89,8 +90,7 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t st)
     // few tokens: their heads spread over more CTAs
     const int gy = std::max(1, std::min((heads + 15) / 16, 296 / gx));
     const int hpc = (heads + gy - 1) / gy;
-    rope_kernel<T, D, TOKENS><<<dim3(gx, (heads + hpc - 1) / hpc), kThreads, 0, st>>>(a, hpc);
-    return cudaGetLastError();
+    return launch_overlapped(rope_kernel<T, D, TOKENS>, dim3(gx, (heads + hpc - 1) / hpc), kThreads, 0, st, a, hpc);
 }
 template <typename T>
 cudaError_t launch(const RopeArgs &a, cudaStream_t st)

@@ -139,6 +139,24 @@ cudaError_t launch_attention(const AttnArgs &a, const SeqLayout &Lq, const SeqLa
                              int *status, cudaStream_t st, sage_status_t *host_err);
 cudaError_t launch_wait_selftest(int *status, uint64_t timeout_ns, cudaStream_t st);
 
+// Launch with programmatic stream serialization: the kernel may start while the one before it
+// in the stream runs down, and calls griddep_wait() before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Host helpers of the C-ABI layer (api.cu): the current device's status word (nullptr and
 // *err on failure), and the status code of a failed CUDA call.
 int *status_ptr(sage_status_t *err);
