@@ -209,10 +209,15 @@ __global__ void __launch_bounds__(kThreads, TOKENS == 1 ? 2 : 3) kv4_append_kern
         cs.load(s_c + tl * half + 8 * u, s_s + tl * half + 8 * u);
 
     if (here && s_w.pos[tl] >= 0) {
-        for (int h = q0 + hl; h < q1; h += kStep) {
+        const T *in = static_cast<const T *>(p.q) + t * p.q_tok + (q0 + hl) * p.q_head;
+        T *out = static_cast<T *>(p.q_out) + t * p.qo_tok + (q0 + hl) * p.qo_head;
+        for (int h = q0 + hl; h < q1; h += kStep, out += kStep * p.qo_head) {
             uint4 w0 = wq[0], w1 = wq[1];
-            if (h + kStep < q1)
-                load(wq, p.q, p.q_tok, p.q_head, h + kStep, ru);
+            in += kStep * p.q_head;
+            if (h + kStep < q1) {
+                wq[0] = *reinterpret_cast<const uint4 *>(in + ru.a0);
+                wq[1] = *reinterpret_cast<const uint4 *>(in + ru.a1);
+            }
             if (ru.rotated) {
                 float f0[8], f1[8];
                 load8<T>(w0, f0);
@@ -221,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, TOKENS == 1 ? 2 : 3) kv4_append_kern
                 w0 = store8<T>(f0);
                 w1 = store8<T>(f1);
             }
-            T *out = static_cast<T *>(p.q_out) + t * p.qo_tok + h * p.qo_head;
             *reinterpret_cast<uint4 *>(out + ru.a0) = w0;
             *reinterpret_cast<uint4 *>(out + ru.a1) = w1;
         }

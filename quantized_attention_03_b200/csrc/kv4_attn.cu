@@ -34,6 +34,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -1027,10 +1028,19 @@ template <int D, int NT, bool FOLD>
 cudaError_t launch(const Params &p, cudaStream_t st)
 {
     using C = Cfg<D, NT, FOLD>;
-    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT, FOLD>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    // once per device: setting it costs a microsecond of every call
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT, FOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess)
+            return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     const int n = C::kCtasPerSM * kSMs;
     e = launch_overlapped(kv4_attn_kernel<D, NT, FOLD>, dim3(n), kThreads, C::kSmem, st, p);
     if (e != cudaSuccess)

@@ -152,12 +152,11 @@ __device__ __forceinline__ void rope_rotate(float (&x)[8], float (&y)[8], const 
     for (int i = 0; i < 4; i++) {
         if (interleaved) {                             // pairs side by side, the unit's 16 channels in a row
             float *v = i < 2 ? x + 4 * i : y + 4 * (i - 2);
-            float2 a = make_float2(v[0], v[2]), b = make_float2(v[1], v[3]);
-            rope_pairs(a, b, cs.c[i], cs.s[i]);
-            v[0] = a.x;
-            v[1] = b.x;
-            v[2] = a.y;
-            v[3] = b.y;
+            const float a = v[0], b = v[1], c = v[2], d = v[3];
+            v[0] = __fsub_rn(__fmul_rn(a, cs.c[i].x), __fmul_rn(b, cs.s[i].x));
+            v[1] = __fadd_rn(__fmul_rn(b, cs.c[i].x), __fmul_rn(a, cs.s[i].x));
+            v[2] = __fsub_rn(__fmul_rn(c, cs.c[i].y), __fmul_rn(d, cs.s[i].y));
+            v[3] = __fadd_rn(__fmul_rn(d, cs.c[i].y), __fmul_rn(c, cs.s[i].y));
         } else {
             float2 a = make_float2(x[2 * i], x[2 * i + 1]), b = make_float2(y[2 * i], y[2 * i + 1]);
             rope_pairs(a, b, cs.c[i], cs.s[i]);
