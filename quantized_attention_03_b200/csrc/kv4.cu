@@ -15,7 +15,7 @@
 namespace sage {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kAppendThreads = 128;   // of gather, and of append
 constexpr int kMaxTokens = 16;    // tokens one CTA takes at most
 
 // The last sequence whose first row is at or before row t (cu non-decreasing), its rows a .. b-1
@@ -63,11 +63,11 @@ __device__ void find_places(const Kv4Seqs &s, int t0, int tokens, int64_t page_b
     // sequence the search below finds for a row
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         int a, b, len;
-        for (int i = threadIdx.x; i < s.nseq; i += kThreads)
+        for (int i = threadIdx.x; i < s.nseq; i += blockDim.x)
             s.rows(i, a, b, len);
     }
     const int warp = threadIdx.x / 32;
-    for (int i = warp; i < tokens; i += kThreads / 32) {
+    for (int i = warp; i < tokens; i += blockDim.x / 32) {
         int a, b, len, pos = -1;
         const int t = t0 + i, seq = find_sequence(s, t, a, b, len);
         int64_t base = -1;
@@ -166,9 +166,9 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float step, floa
 // is computed. Keys and values: the d/16 neighbouring lanes of a head reduce their groups'
 // extremes together and write the codes.
 template <typename T, int D, int TOKENS>
-__global__ void __launch_bounds__(kThreads, TOKENS == 1 ? 2 : 3) kv4_append_kernel(const Kv4AppendArgs p, int q_heads, int kv_heads)
+__global__ void __launch_bounds__(kAppendThreads, TOKENS == 1 ? 4 : 6) kv4_append_kernel(const Kv4AppendArgs p, int q_heads, int kv_heads)
 {
-    constexpr int kUnits = D / 16, kGroups = D / kKv4Group, kStep = kThreads / (TOKENS * kUnits);
+    constexpr int kUnits = D / 16, kGroups = D / kKv4Group, kStep = kAppendThreads / (TOKENS * kUnits);
     // cosines and sines, [TOKENS][rot / 2]
     __shared__ __align__(16) float s_c[TOKENS * D / 2], s_s[TOKENS * D / 2];
     __shared__ Places s_w;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, TOKENS == 1 ? 2 : 3) kv4_append_kern
     find_places(p.s, t0, tokens, page_bytes, s_w);
     __syncthreads();
     const int half = p.rot / 2;
-    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+    for (int i = threadIdx.x; i < tokens * half; i += kAppendThreads) {
         const int k = i / half;
         const float2 cs = rope_cos_sin(s_w.pos[k], __ldg(p.freqs + (i - k * half)), p.mscale, false);
         s_c[i] = cs.x;
@@ -391,13 +391,13 @@ cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
     const int gx = (a.s.total + TOKENS - 1) / TOKENS;
     // few tokens: their heads spread over more CTAs
     const int gy = std::max(1, std::min({((a.q ? a.Hq : 0) + 15) / 16, (a.s.Hkv + 3) / 4, 296 / gx}));
-    return launch_overlapped(kv4_append_kernel<T, D, TOKENS>, dim3(gx, gy), kThreads, 0, st, a, (a.Hq + gy - 1) / gy,
+    return launch_overlapped(kv4_append_kernel<T, D, TOKENS>, dim3(gx, gy), kAppendThreads, 0, st, a, (a.Hq + gy - 1) / gy,
                              (a.s.Hkv + gy - 1) / gy);
 }
 template <typename T>
 cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
 {
-    // with many tokens, as many in a CTA as give its threads an angle each
+    // with many tokens, a few in a CTA: two angles a thread
     if (a.s.total >= 4 * 148)
         return a.d == 128 ? launch_append<T, 128, 4>(a, st) : launch_append<T, 64, 8>(a, st);
     return a.d == 128 ? launch_append<T, 128, 1>(a, st) : launch_append<T, 64, 1>(a, st);

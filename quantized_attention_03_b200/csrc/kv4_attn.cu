@@ -929,9 +929,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
         p.tail[team] = tail;
 }
 
-// Merge of what several teams share: CTA t takes the segment that team t began and did not
-// finish. Its warps take the rows, several a row where the rows are few, eight partials at a
-// time (all their loads in flight together), always in the same order.
+// Merge of what several teams share: a CTA takes the segment that team blockIdx.x began and did
+// not finish, or, where teams are warps and rows at most 8, each half of it one such segment; a
+// segment of many CTAs has several CTAs here, a slice of the rows each.
+// Its warps take the rows, several a row where the rows are few, eight partials at a time (all
+// their loads in flight together), always in the same order.
 template <int D, int NT, bool FOLD>
 __global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params p)
 {
@@ -941,17 +943,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params 
     __shared__ float2 s_ml[kMergeWarps];
     griddep_launch_dependents();
     griddep_wait();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, team = blockIdx.x;
-    if (*p.solo == 0 && team >= gridDim.x / kWarps)
-        return;
+    const int lane = threadIdx.x % 32, slot_warp = threadIdx.x / 32;
+    const bool solo = *p.solo != 0;
+    const int mine = solo && C::kRows <= 8 ? kMergeWarps / 2 : kMergeWarps;   // warps of a segment
+    const int teams = C::kCtasPerSM * kSMs;            // of CTAs; their rows go to several CTAs each
+    const int team = solo ? blockIdx.x * (kMergeWarps / mine) + slot_warp / mine : blockIdx.x % teams;
+    const int warp = slot_warp % mine;
     const Tail t = p.tail[team];
     if (t.last < 0)
         return;
-    const int r0 = t.rb * C::kRows, nrows = min(C::kRows, t.n * p.group - r0);
-    const int split = nrows <= 1 ? 8 : nrows <= 2 ? 4 : nrows <= 4 ? 2 : 1;   // warps of a row
+    const int r0 = t.rb * C::kRows;
+    int first = 0, nrows = min(C::kRows, t.n * p.group - r0);
+    if (!solo) {
+        const int slices = gridDim.x / teams, rows = (nrows + slices - 1) / slices;
+        first = blockIdx.x / teams * rows;
+        nrows = min(nrows, first + rows);
+    }
+    const int count = nrows - first;
+    if (count <= 0)
+        return;
+    const int split = count <= mine / 8 ? 8 : count <= mine / 4 ? 4 : count <= mine / 2 ? 2 : 1;   // warps of a row
     const int each = (t.last - team + split) / split, part = warp % split;
     const int c0 = team + part * each, c1 = min(t.last + 1, c0 + each);
-    for (int base = 0; base < nrows; base += kMergeWarps / split) {
+    for (int base = first; base < nrows; base += mine / split) {
         const int r = base + warp / split;
         float M = -INFINITY, L = 0.0f, acc[kC] = {};
         for (int c = c0; r < nrows && c < c1; c += kChunk) {
@@ -989,16 +1003,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params 
                     acc[k] = fmaf(w, c + i < c1 ? v[i][k] : 0.0f, acc[k]);
             }
         }
-        if (split > 1) {
-            __syncthreads();
-            s_ml[warp] = make_float2(M, L);
+        if (split > 1) {                               // and then the loop ends here: one barrier is enough
+            s_ml[slot_warp] = make_float2(M, L);
 #pragma unroll
             for (int k = 0; k < kC; k++)
-                s_part[warp][lane * kC + k] = acc[k];
-            __syncthreads();
+                s_part[slot_warp][lane * kC + k] = acc[k];
+            named_bar_sync(1 + slot_warp / mine, mine * 32);
             if (part)
                 continue;
-            for (int w = warp + 1; w < warp + split; w++) {
+            for (int w = slot_warp + 1; w < slot_warp + split; w++) {
                 const float2 o = s_ml[w];
                 const float m = fmaxf(M, o.x), b = m == -INFINITY ? 0.0f : m;
                 const float sa = ex2_approx(M - b), sb = ex2_approx(o.x - b);
@@ -1045,7 +1058,8 @@ cudaError_t launch(const Params &p, cudaStream_t st)
     e = launch_overlapped(kv4_attn_kernel<D, NT, FOLD>, dim3(n), kThreads, C::kSmem, st, p);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(kv4_attn_merge<D, NT, FOLD>, dim3(n * kWarps), kMergeWarps * 32, 0, st, p);
+    return launch_overlapped(kv4_attn_merge<D, NT, FOLD>, dim3(C::kRows <= 8 ? n * kWarps / 2 : n * kWarps),
+                             kMergeWarps * 32, 0, st, p);
 }
 
 // [whether solo | tails], then the partial rows, of as many teams as there are warps
