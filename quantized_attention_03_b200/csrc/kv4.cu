@@ -27,22 +27,22 @@ __device__ int find_sequence(const Kv4Seqs &s, int t, int &a, int &b, int &len)
         const int n = s.total / s.nseq, seq = min(t / n, s.nseq - 1);
         a = seq * n;
         b = a + n;
-        len = __ldg(s.kv_lens + seq);
+        len = s.kv_lens[seq];
         return seq;
     }
     const int lane = threadIdx.x % 32;
     int lo = 0, n = s.nseq;                            // the answer is in [lo, lo + n)
     while (n > 32) {
         const int step = (n + 31) / 32;
-        const bool le = lane * step < n && __ldg(s.cu + lo + lane * step) <= t;
+        const bool le = lane * step < n && s.cu[lo + lane * step] <= t;
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
         lo += last * step;
         n = min(step, n - last * step);
     }
     const int i = lo + min(lane, n - 1);
-    a = __ldg(s.cu + i);
-    b = __ldg(s.cu + i + 1);
-    len = __ldg(s.kv_lens + i);
+    a = s.cu[i];
+    b = s.cu[i + 1];
+    len = s.kv_lens[i];
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, lane < n && a <= t) | 1u);
     a = __shfl_sync(0xffffffffu, a, last);
     b = __shfl_sync(0xffffffffu, b, last);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kAppendThreads, TOKENS == 1 ? 4 : 6) kv4_appen
     const int half = p.rot / 2;
     for (int i = threadIdx.x; i < tokens * half; i += kAppendThreads) {
         const int k = i / half;
-        const float2 cs = rope_cos_sin(s_w.pos[k], __ldg(p.freqs + (i - k * half)), p.mscale, false);
+        const float2 cs = rope_cos_sin(s_w.pos[k], p.freqs[i - k * half], p.mscale, false);
         s_c[i] = cs.x;
         s_s[i] = cs.y;
     }
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(kAppendThreads, TOKENS == 1 ? 4 : 6) kv4_appen
                     const float2 *m1 = reinterpret_cast<const float2 *>(p.k_mean + h * D + a1);
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const float2 x = sub2(make_float2(f0[2 * j], f0[2 * j + 1]), __ldg(m0 + j));
-                        const float2 y = sub2(make_float2(f1[2 * j], f1[2 * j + 1]), __ldg(m1 + j));
+                        const float2 x = sub2(make_float2(f0[2 * j], f0[2 * j + 1]), m0[j]);
+                        const float2 y = sub2(make_float2(f1[2 * j], f1[2 * j + 1]), m1[j]);
                         f0[2 * j] = x.x;
                         f0[2 * j + 1] = x.y;
                         f1[2 * j] = y.x;
@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4GatherArg
                 o[i] = ((int64_t)(t0 + tl) * Hkv + h) * p.rep * D + wd * 8;
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
-                    w[i][x] = __ldg(reinterpret_cast<const uint32_t *>(page + (x * ps + row) * (D / 2)) + wd);
-                    sl[i][x] = __ldg(reinterpret_cast<const __half2 *>(page + ps * D + (x * ps + row) * (kGroups * 4)) +
+                    w[i][x] = reinterpret_cast<const uint32_t *>(page + (x * ps + row) * (D / 2))[wd];
+                    sl[i][x] = *(reinterpret_cast<const __half2 *>(page + ps * D + (x * ps + row) * (kGroups * 4)) +
                                      wd / 8);
                 }
             }

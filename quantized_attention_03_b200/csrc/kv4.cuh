@@ -46,14 +46,14 @@ struct Kv4Seqs {
     __device__ bool rows(int s, int &a, int &b, int &len) const
     {
         if (cu) {
-            a = __ldg(cu + s);
-            b = __ldg(cu + s + 1);
+            a = cu[s];
+            b = cu[s + 1];
         } else {
             const int n = total / nseq;
             a = s * n;
             b = a + n;
         }
-        len = __ldg(kv_lens + s);
+        len = kv_lens[s];
         if (sound(a, b, len))
             return true;
         a = b = len = 0;
@@ -69,7 +69,7 @@ struct Kv4Seqs {
     // Page of token j of sequence s, or -1 (and a status bit) if the table's entry is not one.
     __device__ int page(int s, int j) const
     {
-        const int id = __ldg(block_table + (int64_t)s * max_pages + (j >> page_log2));
+        const int id = block_table[(int64_t)s * max_pages + (j >> page_log2)];
         if (id < 0 || id >= num_pages) {
             atomicOr(status, status_bit(SAGE_ERR_BAD_PAGE));
             return -1;

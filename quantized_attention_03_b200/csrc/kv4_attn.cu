@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
         const int key = next_tile * C::kTile + lane * slice;
         ids = 0;
         if (more && lane * slice < C::kTile && key < keys)
-            ids = __ldg(table + (key >> sq.page_log2));
+            ids = table[key >> sq.page_log2];
     };
     auto issue = [&]() {
         if (more) {
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             for (int gr = 0; gr < kG; gr++)
 #pragma unroll
                 for (int j = 0; j < 2; j++)
-                    u[gr][j] = r < nrows ? __ldg(reinterpret_cast<const uint4 *>(src + gr * 64) + j)
+                    u[gr][j] = r < nrows ? reinterpret_cast<const uint4 *>(src + gr * 64)[j]
                                          : make_uint4(0u, 0u, 0u, 0u);
             f[i][0] = f[i][1] = query_row<kG>(u, p.a.bf16, qf[i]);
             f[i][0] = __shfl_sync(0xffffffffu, f[i][0], t4 * 8) * p.sc_log2;

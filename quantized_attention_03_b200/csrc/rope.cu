@@ -28,8 +28,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs p, int
     const int half = p.rot / 2, all = p.B * p.N, t0 = blockIdx.x * TOKENS;
     for (int i = threadIdx.x; i < TOKENS * half; i += kThreads) {
         const int t = min(t0 + i / half, all - 1), b = t / p.N, n = t - b * p.N;
-        const int pos = p.positions ? __ldg(p.positions + b * p.pos_b + n) : n;
-        const float2 cs = rope_cos_sin(pos, __ldg(p.freqs + i % half), p.mscale, p.inverse);
+        const int pos = p.positions ? p.positions[b * p.pos_b + n] : n;
+        const float2 cs = rope_cos_sin(pos, p.freqs[i % half], p.mscale, p.inverse);
         s_c[i] = cs.x;
         s_s[i] = cs.y;
     }

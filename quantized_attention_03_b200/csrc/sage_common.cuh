@@ -140,7 +140,10 @@ cudaError_t launch_attention(const AttnArgs &a, const SeqLayout &Lq, const SeqLa
 cudaError_t launch_wait_selftest(int *status, uint64_t timeout_ns, cudaStream_t st);
 
 // Launch with programmatic stream serialization: the kernel may start while the one before it
-// in the stream runs down, and calls griddep_wait() before it touches memory.
+// in the stream runs down, and calls griddep_wait() before it touches memory. Every thread
+// calls it (also one that has nothing to do: the kernel after this one waits for this one
+// alone), and memory that the kernel before may have written is read with plain loads, not
+// through the read-only path.
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
 {
