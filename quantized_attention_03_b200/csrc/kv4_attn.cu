@@ -166,9 +166,11 @@ __device__ __forceinline__ void write_row(const Kv4AttnArgs &a, int64_t row, int
 // the 16-bit input. Operand 0 of an 8-channel word is channels (0, 4), 1 is (1, 5) / 16, 2 is
 // (2, 6), 3 is (3, 7) / 16, as the masked codes have them. The row is scaled by a power of two
 // so that its largest element is in [2^14, 2^15); returned is what a product's units are worth,
-// 2^24 over that factor (the codes are 2^-24).
+// 2^24 over that factor (the codes are 2^-24), and in those units the row's sum over each group
+// (in fp32: products of subnormals keep 2^-18 of their size, too little for the one term that
+// all keys share).
 template <int G>
-__device__ __forceinline__ float query_row(const uint4 (&u)[G][2], int bf16, uint32_t (&qf)[G][2][4])
+__device__ __forceinline__ float query_row(const uint4 (&u)[G][2], int bf16, uint32_t (&qf)[G][2][4], float (&sum)[G])
 {
     float big;
     if (bf16) {
@@ -188,8 +190,12 @@ __device__ __forceinline__ float query_row(const uint4 (&u)[G][2], int bf16, uin
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
     const int e = max(-100, min(100, (int)(__float_as_uint(big) >> 23) - 127));
     const float scale = __uint_as_float((uint32_t)(127 + 14 - e) << 23), s16 = scale * 0.0625f;
+    // 2^(24 - 14 + e) and its reciprocal
+    const float unit = __uint_as_float((uint32_t)(127 + 10 + e) << 23);
+    const float per = __uint_as_float((uint32_t)(127 - 10 - e) << 23);
 #pragma unroll
-    for (int gr = 0; gr < G; gr++)
+    for (int gr = 0; gr < G; gr++) {
+        sum[gr] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             float w[8];
@@ -201,8 +207,12 @@ __device__ __forceinline__ float query_row(const uint4 (&u)[G][2], int bf16, uin
             qf[gr][j][1] = pack_half2(w[1] * s16, w[5] * s16);
             qf[gr][j][2] = pack_half2(w[2] * scale, w[6] * scale);
             qf[gr][j][3] = pack_half2(w[3] * s16, w[7] * s16);
+            sum[gr] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
         }
-    return __uint_as_float((uint32_t)(127 + 10 + e) << 23);   // 2^(24 - 14 + e)
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+        sum[gr] = (sum[gr] + __shfl_xor_sync(0xffffffffu, sum[gr], 2)) * per;
+    }
+    return unit;
 }
 
 // Segments of a sequence (key heads x row blocks) and tiles of each; at least one tile where it
@@ -513,26 +523,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 for (int j = 0; j < 2; j++)
                     u[gr][j] = r < nrows ? reinterpret_cast<const uint4 *>(src + gr * 64)[j]
                                          : make_uint4(0u, 0u, 0u, 0u);
-            f[i][0] = f[i][1] = query_row<kG>(u, p.a.bf16, qf[i]);
+            float sum[kG];
+            f[i][0] = f[i][1] = query_row<kG>(u, p.a.bf16, qf[i], sum);
+#pragma unroll
+            for (int gr = 0; gr < kG; gr++) {
+                qs[i][gr][0] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8);
+                qs[i][gr][1] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8 + 4);
+            }
             f[i][0] = __shfl_sync(0xffffffffu, f[i][0], t4 * 8) * p.sc_log2;
             f[i][1] = __shfl_sync(0xffffffffu, f[i][1], t4 * 8 + 4) * p.sc_log2;
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 const int rr = FOLD ? (2 * t4 + c) % 4 : i * 8 + 2 * t4 + c;
                 lim[i][c] = p.a.causal && rr < nrows ? len - seg.n + (r0 + rr) / p.group : len - 1;
-            }
-            // a row's sum over a group's channels, in the products' own units: codes that are all 1
-#pragma unroll
-            for (int gr = 0; gr < kG; gr++) {
-                float one[4] = {};
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-#pragma unroll
-                    for (int hf = 0; hf < 2; hf++)
-                        mma16816(one, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qf[i][gr][j][2 * hf],
-                                 qf[i][gr][j][2 * hf + 1]);
-                qs[i][gr][0] = one[0];
-                qs[i][gr][1] = one[1];
             }
         }
         // keys up to here are seen by every row of the block

@@ -6,7 +6,7 @@
 // The angle, its sine and its cosine are 64-bit (p f_i reaches 10^6 and more, where a
 // 32-bit angle is wrong by 0.06 and more) and rounded once to 32 bits with the factor m;
 // the rotation itself is four 32-bit products and two sums, each rounded on its own (no
-// fused multiply-add, except by -1), so that the codes the cache gets from it are defined bit for bit.
+// fused multiply-add), so that the codes the cache gets from it are defined bit for bit.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -136,11 +136,12 @@ struct RopeAngles {
     }
 };
 
-// Rotates two pairs, (a.x, b.x) and (a.y, b.y): a <- a c - b s, b <- b c + a s.
-__device__ __forceinline__ void rope_pairs(float2 &a, float2 &b, float2 c, float2 s)
+// Rotates a pair: a <- a c - b s, b <- b c + a s. (Packed pairs of these lose the rounding of
+// the products: mul and add of f32x2 were fused on the way, one result in 2^14 differed.)
+__device__ __forceinline__ void rope_pair(float &a, float &b, float c, float s)
 {
-    const float2 x = sub2(mul2(a, c), mul2(b, s));
-    b = add2(mul2(b, c), mul2(a, s));
+    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
     a = x;
 }
 
@@ -152,18 +153,11 @@ __device__ __forceinline__ void rope_rotate(float (&x)[8], float (&y)[8], const 
     for (int i = 0; i < 4; i++) {
         if (interleaved) {                             // pairs side by side, the unit's 16 channels in a row
             float *v = i < 2 ? x + 4 * i : y + 4 * (i - 2);
-            const float a = v[0], b = v[1], c = v[2], d = v[3];
-            v[0] = __fsub_rn(__fmul_rn(a, cs.c[i].x), __fmul_rn(b, cs.s[i].x));
-            v[1] = __fadd_rn(__fmul_rn(b, cs.c[i].x), __fmul_rn(a, cs.s[i].x));
-            v[2] = __fsub_rn(__fmul_rn(c, cs.c[i].y), __fmul_rn(d, cs.s[i].y));
-            v[3] = __fadd_rn(__fmul_rn(d, cs.c[i].y), __fmul_rn(c, cs.s[i].y));
+            rope_pair(v[0], v[1], cs.c[i].x, cs.s[i].x);
+            rope_pair(v[2], v[3], cs.c[i].y, cs.s[i].y);
         } else {
-            float2 a = make_float2(x[2 * i], x[2 * i + 1]), b = make_float2(y[2 * i], y[2 * i + 1]);
-            rope_pairs(a, b, cs.c[i], cs.s[i]);
-            x[2 * i] = a.x;
-            x[2 * i + 1] = a.y;
-            y[2 * i] = b.x;
-            y[2 * i + 1] = b.y;
+            rope_pair(x[2 * i], y[2 * i], cs.c[i].x, cs.s[i].x);
+            rope_pair(x[2 * i + 1], y[2 * i + 1], cs.c[i].y, cs.s[i].y);
         }
     }
 }
