@@ -2,6 +2,7 @@
 of the C entry points and of the wrappers, all of which happen before any CUDA call."""
 import ctypes
 import math
+import sys
 
 import pytest
 import torch
@@ -211,3 +212,24 @@ def test_wrappers_refuse_wrong_tensors_before_the_library(lib):
         with pytest.raises(ValueError):
             call()
             raise AssertionError(i)
+
+
+def test_tensors_of_the_cpu_are_refused(lib):
+    cache, table, lens, cu = _cpu_sequences()
+    f, _ = sage.rope_freqs(64, device="cpu")
+    k = torch.zeros((2, 2, 64), dtype=torch.float16)
+    for call in (lambda: sage.rope(k, None, f), lambda: sage.kv4_append(cache, table, lens, cu, k, k, None, f),
+                 lambda: sage.kv4_gather(cache, table, lens, cu, 2, 64),
+                 lambda: sage.attn_kv4(k, cache, table, lens, cu, 1)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    with pytest.raises(ValueError, match="is a tensor"):
+        sage.rope([1.0], None, f)
+
+
+def test_missing_binding_fails_loudly(lib, monkeypatch):
+    monkeypatch.setattr(sage, "_calls", None)
+    monkeypatch.delattr(sage, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, "quantized_attention_03_b200._binding", None)
+    with pytest.raises(RuntimeError, match="_binding.so"):
+        sage.rope(torch.zeros((1, 1, 64), dtype=torch.float16), None, torch.zeros(32, dtype=torch.float64))

@@ -3,9 +3,10 @@
 Tolerances. A rounding to the output's type is off by at most half a step, 2^-11 (fp16) or
 2^-8 (bf16) of the value. The rotation's 32-bit steps add at most 4 2^-24 (|x0| + |x1|) m: a
 sine or cosine rounded once, a product, a sum. Codes and params are defined in 32-bit steps
-and have to be equal. Attention's 32-bit steps: a score is a sum over d channels in at most 20
-accumulations of at most 2^-23 of the terms' absolute sum, so it is off by less than 2^-18 of
-that sum; probabilities follow their scores, and carry 2^-21 of their own (two fp16 terms, the
+and have to be equal. Attention's steps: a score is a sum over d channels in at most 20
+accumulations; codes enter as fp16 subnormals, whose products are aligned with up to 10 leading
+zeros, so each is good to 2^-24 + 10 / 4 bits of the terms' absolute sum and the score to less
+than 2^-18 of it; probabilities follow their scores, and carry 2^-21 of their own (two fp16 terms, the
 exponential); summing n keys in 32 bits adds at most 2^-23 per 16 keys.
 """
 import math
@@ -73,6 +74,19 @@ def test_rope(B, Hq, Hk, N, d, rot, inter, inv, dt):
         want = want.unflatten(0, (B, N)).transpose(1, 2)
         near(y, want, 4 * 2.0 ** -24 * 2 * m * x.double().abs().amax())
         assert torch.equal(y.cpu()[..., rot:], x[..., rot:])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 128), (128, 48)])
+def test_rope_is_the_defined_arithmetic(d, rot, inter):
+    # sines and cosines rounded once to fp32, then products and sums each rounded: bit for bit
+    g = torch.Generator().manual_seed(rot)
+    x = torch.randn((640, 5, d), generator=g).to(F16)
+    pos = torch.randint(0, 100000, (640,), generator=g, dtype=torch.int32)
+    freqs, m = sage.rope_freqs(rot, scaling="parts", factor=8.0, original_len=4096)
+    got, _ = sage.rope(x.cuda(), None, freqs, pos.cuda(), m, inter)
+    ok()
+    assert torch.equal(got.cpu(), ref.rotate(x, pos, freqs.cpu(), m, inter, dtype=torch.float32).to(F16))
 
 
 def test_rope_views_in_place_and_packed():
@@ -244,6 +258,20 @@ def test_gather(lens, news, Hq, Hkv, d, page, dt, rep):
             assert (out[T:] == 9.0).all()
 
 
+def test_append_rotates_queries_in_place():
+    w = World([30, 900], [30, 700], 2, 64, 32, seed=1)
+    fused = torch.randn((w.total, 8, 64), generator=w.g).to(BF16).cuda()
+    freqs, m = sage.rope_freqs(64)
+    where = w.where()
+    a, b = w.cache.cuda(), w.cache.cuda()
+    want = sage.kv4_append(a, *where, fused[:, 4:6], fused[:, 6:], fused[:, :4], freqs, m)
+    kv = fused[:, 4:].clone()
+    got = sage.kv4_append(b, *where, fused[:, 4:6], fused[:, 6:], fused[:, :4], freqs, m, q_out=fused[:, :4])
+    ok()
+    assert torch.equal(got, want) and torch.equal(fused[:, :4], want)
+    assert torch.equal(a, b) and torch.equal(fused[:, 4:], kv)
+
+
 # ------------------------------------------------------------------------- attention
 
 
@@ -294,6 +322,54 @@ def test_attention(lens, news, Hq, Hkv, d, page, dt, causal):
     ok()
     assert got is out and (out[w.total:] == 5.0).all() and (lse[w.total:] == 5.0).all()
     check_attn(w, q[:w.total], out, lse, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,new", [(4, 1), (8, 1), (4, 5)])
+def test_attention_of_many_segments(group, new, d):
+    # from 148 (sequence, key head, row block) on, warps work alone; rows 4, 8 and 20 of a key head
+    g = torch.Generator().manual_seed(group + new)
+    lens = torch.randint(0, 900, (26,), generator=g).tolist()
+    news = [min(n, int(x)) for n, x in zip(lens, torch.randint(new > 1 and 0 or 1, new + 1, (26,), generator=g))]
+    w = World(lens, news, 8, d, 32, seed=13)
+    w.fill()
+    q = torch.randn((w.total, 8 * group, d), generator=w.g).to(F16)
+    lse = torch.empty((w.total, 8 * group), device="cuda")
+    out = sage.attn_kv4(q.cuda(), w.cache.cuda(), *w.where(), new, lse=lse)
+    ok()
+    check_attn(w, q, out, lse)
+
+
+def test_attention_over_shared_pages():
+    # three sequences that begin with the same pages (a common prompt) and end in their own
+    w = World([100, 90, 64], [1, 1, 1], 2, 64, 32, seed=14)
+    w.fill()
+    w.table[1, :2] = w.table[0, :2]
+    w.table[2, :2] = w.table[0, :2]
+    q = torch.randn((3, 4, 64), generator=w.g).to(F16)
+    out = sage.attn_kv4(q.cuda(), w.cache.cuda(), *w.where(), 1)
+    ok()
+    check_attn(w, q, out, None)
+
+
+def test_two_calls_at_once():
+    # the same cache read by two streams at a time, a workspace each
+    w = World([2000, 900, 1500, 40] * 8, [1] * 32, 8, 128, 16, seed=15)
+    w.fill()
+    qs = [torch.randn((32, h, 128), generator=w.g).to(F16).cuda() for h in (32, 64)]
+    cache, where = w.cache.cuda(), w.where()
+    want = [sage.attn_kv4(q, cache, *where, 1) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(sage.attn_kv4(qs[i], cache, *where, 1))
+    torch.cuda.synchronize()
+    ok()
+    for i in (0, 1):
+        assert all(torch.equal(x, want[i]) for x in got[i])
 
 
 @pytest.mark.parametrize("d", [64, 128])
