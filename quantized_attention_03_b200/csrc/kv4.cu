@@ -16,7 +16,7 @@ namespace sage {
 namespace {
 
 constexpr int kThreads = 256, kAppendThreads = 128;   // of gather, and of append
-constexpr int kMaxTokens = 16;    // tokens one CTA takes at most
+constexpr int kMaxTokens = 8;     // tokens one CTA takes at most, a warp each to find their places
 
 // The last sequence whose first row is at or before row t (cu non-decreasing), its rows a .. b-1
 // and its length, found by a whole warp: each round looks at 32 spread places at once, and the
@@ -397,8 +397,9 @@ cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
 template <typename T>
 cudaError_t launch_append(const Kv4AppendArgs &a, cudaStream_t st)
 {
-    // with many tokens, a few in a CTA: two angles a thread
-    if (a.s.total >= 4 * 148)
+    // with many tokens, a few in a CTA: 32 + 16 heads of d = 128 take 13 us one a CTA and 18 four a
+    // CTA for 1024 tokens, 50 and 43 for 4096
+    if (a.s.total >= 16 * 148)
         return a.d == 128 ? launch_append<T, 128, 4>(a, st) : launch_append<T, 64, 8>(a, st);
     return a.d == 128 ? launch_append<T, 128, 1>(a, st) : launch_append<T, 64, 1>(a, st);
 }
@@ -411,7 +412,10 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs &a, cudaStream_t st)
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, cudaStream_t st)
 {
-    const int tpc = a.s.total >= 8 * 4 * 148 ? 8 : 1;
+    // tokens of a CTA: about 2048 stores of 16 bytes, but at least 2 CTAs an SM. 16384 tokens of 8
+    // heads, each written 4 times: 48 us with 2 tokens, 51 with 8; once: 26 and 20
+    const int stores = a.s.Hkv * (a.d / 8) * a.rep * 2;
+    const int tpc = std::max(1, std::min({kMaxTokens, std::max(2, 2048 / stores), a.s.total / 592}));
     const int grid = (a.s.total + tpc - 1) / tpc;
     auto go = [&](auto kern) { return launch_overlapped(kern, dim3(grid), kThreads, 0, st, a, tpc); };
     if (a.bf16)

@@ -7,16 +7,18 @@
 // two 16-bit tensor-core products and the params scale their 32-bit results (keys) or the
 // probabilities (values).
 //
-// What bounds it: the cache is read once from HBM, 0.5625 bytes per element, and each
-// element has to be turned from 4 bits into a 16-bit operand, so the instructions that
-// unpack (0.6 per key element, 0.9 per value element) are the second bound.
+// What bounds it: the cache is read once from HBM, 0.5625 bytes per element (B8 H32 over 32768
+// keys of d 128: 1.21 GB, 185 us at the copy bandwidth, which the copies alone reach), and each
+// element has to be turned from 4 bits into a 16-bit operand: the instructions are the bound,
+// 231 us for that cache without its copies, 250 us in all (4.8 TB/s).
 //   - A code masked in place is an fp16 subnormal, n 2^-24 or 16 n 2^-24, which the tensor core
-//     multiplies exactly; one AND makes two operands. The queries of the second kind of channel
-//     are divided by 16 beforehand, the outputs' at the end.
+//     takes as it is; one AND makes two operands. The queries of the second kind of channel are
+//     divided by 16 beforehand, the outputs at the end. Sums of such products are good to 2^-18.
 //   - Values are centred (n - 8), because the sum of p n' stays near the size of its result;
 //     uncentred it would be the difference of two sums 100 times larger over a long cache, in
 //     which the accumulator's own rounding shows. One product with constant codes -8 gives what
-//     a tile has to be lessened by, the same for all channels.
+//     a tile has to be lessened by, the same for all channels (centring the codes themselves,
+//     an addition for every two, took 260 us).
 //   - Probabilities times step are split into two fp16 terms, high and low, each with its own
 //     product: one term alone would round every p to 11 bits, as much error again as the
 //     rounding of the 16-bit output.
@@ -26,11 +28,12 @@
 // memory, expanded to bytes.
 //
 // Work split: all (sequence, key head, row block, tile) of the call form one list, cut into
-// equal shares, one per CTA, whatever the sequences' lengths (which only the device knows);
-// the eight warps of a CTA take the share's tiles in turn, each through its own ring of
-// copies, and are merged at the end of every (sequence, head). What a CTA began or
-// left unfinished goes to two partial slots of the workspace and a second kernel merges
-// those in order, so results do not depend on timing.
+// equal shares whatever the sequences' lengths (which only the device knows), one per team: a
+// warp where there are many such segments, else a CTA, whose warps take its tiles in turn. Each
+// warp fetches its tiles through a ring of its own, up to two ahead and across segments; a CTA's
+// warps are merged at the end of every segment. What a team began or left unfinished goes to two
+// partial slots of the workspace and a second kernel merges those in order, so results do not
+// depend on timing.
 #include <math.h>
 
 #include <algorithm>
@@ -49,9 +52,14 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMergeWarps = 8;
 constexpr int kSMs = 148;
 // Places that the start of a segment takes in the list of work, in tiles: what it costs a CTA
-// to start on one (queries, pages, first tile, merge), or a warp that works alone.
+// to start on one (queries, pages, first tile, merge), or a warp that works alone. Without it, a
+// CTA that gets many short sequences is the last to end: 64 sequences of 1 to 8192 tokens took
+// 122 us with 0, 101 with 8, 93 with 16, 95 with 24.
 constexpr int kTeamCost = 16, kSoloCost = 2;
-// From so many segments on, every warp works alone on its own share; below, a CTA's warps share one.
+// From so many segments on, every warp works alone on its own share (64 such sequences 84 against
+// 95 us, 256 of up to 200 tokens 31 against 42); below, the warps of a CTA share one, since the
+// partial rows of all warps for one segment would cost more than its keys (8 segments of 32768
+// keys: 53 against 23 us).
 constexpr int kSoloSegments = kSMs;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,7 +72,9 @@ struct Cfg {
     static constexpr int kTile = 4096 / D;             // keys per warp tile
     static constexpr int kGroups = D / kKv4Group;
     static constexpr int kStages = NT == 1 ? 2 : 3;
-    static constexpr int kCtasPerSM = NT == 1 ? 3 : 2;   // 168 or 255 registers a thread
+    // 12 warps of 168 registers or 8 of 255; 16 of 128 registers spill: 98 against 86 us over the
+    // ragged sequences below
+    static constexpr int kCtasPerSM = NT == 1 ? 3 : 2;
     static constexpr int kRows = FOLD ? 4 : 8 * NT;
     static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
     static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
@@ -73,8 +83,8 @@ struct Cfg {
     static constexpr int kSmem = kRing + kWarps * kRows * kPitch * 4;
 };
 
-// What a CTA that begins a (sequence, head, row block) and does not finish it leaves for the
-// merge: the last CTA that works on it (-1: nothing to merge) and whose rows they are.
+// What a team that begins a (sequence, head, row block) and does not finish it leaves for the
+// merge: the last team that works on it (-1: nothing to merge) and whose rows they are.
 struct Tail {
     int last, row0, n, kvh, rb;
 };
@@ -400,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
     }
     __syncthreads();
 
-    // ---- the warp's ring of tiles, filled by 16-byte asynchronous copies of all its lanes (a
-    // bulk copy per page takes its operands from the warp, not the lane: 15% slower here)
+    // ---- the warp's ring of tiles, filled by 16-byte asynchronous copies of all its lanes (bulk
+    // copies take their operands from the warp, so lanes that copy a page each issue in turn: 6%
+    // slower)
     uint8_t *ring = smem + warp * (C::kStages * C::kStageBytes);
     const uint32_t ring_at = smem_u32(ring) + lane * 16;
     const int ps = sq.page_size();
@@ -1032,6 +1043,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params 
 }
 
 // What takes a call's rows per key head: the folded tile up to 4, one tile up to 8, else two.
+// Of the longest cache below, one row takes 252 us folded and 284 in a plain tile; 16 rows of 64
+// sequences take 147 us in two tiles and 175 in two passes of one.
 int variant(int Hq, int Hkv, int max_q)
 {
     const int rows = max_q * (Hq / Hkv);
