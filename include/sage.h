@@ -327,7 +327,10 @@ SAGE_API sage_status_t sage_attn_decode_quantized(const int8_t *q_i8, const floa
  * keys and writes keys and values into a paged cache in 4 bits; sage_attn_kv4 is the
  * attention of a few new queries per sequence over that cache; sage_kv4_gather reads the
  * cache back as 16-bit tensors, e.g. for sage_attn_varlen_fwd_kv of a prefill chunk.
- * Tensors are fp16 (dtype SAGE_F16) or bf16 (SAGE_BF16), head dim 64 or 128.
+ * Tensors are fp16 (dtype SAGE_F16) or bf16 (SAGE_BF16), head dim 64 or 128. Nothing here
+ * allocates; make the first call on each device before any stream capture. Kernels may start
+ * while the one before them in the stream runs down (programmatic stream serialization) and
+ * wait for it before they touch memory.
  *
  * Rotation: pair i of the first rot_dim channels of a head at position p becomes
  * y0 = x0 c - x1 s, y1 = x1 c + x0 s, c = cos(p freqs[i]) mscale, s = sin(p freqs[i])
