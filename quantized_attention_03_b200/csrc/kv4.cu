@@ -303,16 +303,21 @@ __global__ void __launch_bounds__(kAppendThreads, TOKENS == 1 ? 4 : 6) kv4_appen
             uint8_t *codes = page + (is_v ? ps * (D / 2) : 0) + row * (D / 2);
             __half2 *params = reinterpret_cast<__half2 *>(page + ps * D + (is_v ? ps * kGroups * 4 : 0)) +
                               row * kGroups;
-            auto store = [&](const float (&f)[8], int a, float lo, float hi) {
+            auto word = [&](const float (&f)[8], int a, float lo, float hi) {
                 const __half step = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
                 const __half low = __float2half_rn(lo);
                 const float sf = __half2float(step);
-                *reinterpret_cast<uint32_t *>(codes + a / 2) = codes8(f, sf, __half2float(low), __frcp_rn(sf));
                 if (a % kKv4Group == 0)                // the chunk that begins a group writes its params
                     params[a / kKv4Group] = __halves2half2(step, low);
+                return codes8(f, sf, __half2float(low), __frcp_rn(sf));
             };
-            store(f0, a0, lo0, hi0);
-            store(f1, a1, lo1, hi1);
+            const uint32_t w0 = word(f0, a0, lo0, hi0), w1 = word(f1, a1, lo1, hi1);
+            if (is_v || a1 == a0 + 8) {
+                *reinterpret_cast<uint2 *>(codes + a0 / 2) = make_uint2(w0, w1);
+            } else {
+                *reinterpret_cast<uint32_t *>(codes + a0 / 2) = w0;
+                *reinterpret_cast<uint32_t *>(codes + a1 / 2) = w1;
+            }
         }
     };
     walk(std::false_type{}, wk, p.k, p.k_tok, p.k_head);

@@ -149,13 +149,17 @@ __device__ __forceinline__ void rope_pair(float &a, float &b, float c, float s)
 __device__ __forceinline__ void rope_rotate(float (&x)[8], float (&y)[8], const RopeAngles &cs,
                                             bool interleaved)
 {
+    if (interleaved) {                                 // pairs side by side, the unit's 16 channels in a row
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        if (interleaved) {                             // pairs side by side, the unit's 16 channels in a row
-            float *v = i < 2 ? x + 4 * i : y + 4 * (i - 2);
-            rope_pair(v[0], v[1], cs.c[i].x, cs.s[i].x);
-            rope_pair(v[2], v[3], cs.c[i].y, cs.s[i].y);
-        } else {
+        for (int i = 0; i < 2; i++) {
+            rope_pair(x[4 * i], x[4 * i + 1], cs.c[i].x, cs.s[i].x);
+            rope_pair(x[4 * i + 2], x[4 * i + 3], cs.c[i].y, cs.s[i].y);
+            rope_pair(y[4 * i], y[4 * i + 1], cs.c[2 + i].x, cs.s[2 + i].x);
+            rope_pair(y[4 * i + 2], y[4 * i + 3], cs.c[2 + i].y, cs.s[2 + i].y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
             rope_pair(x[2 * i], y[2 * i], cs.c[i].x, cs.s[i].x);
             rope_pair(x[2 * i + 1], y[2 * i + 1], cs.c[i].y, cs.s[i].y);
         }
