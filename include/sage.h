@@ -443,7 +443,7 @@ SAGE_API sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_t
  * A query that sees no key gets zeros and -inf. sm_scale <= 0 selects 1/sqrt(d). Scores and
  * softmax are fp32; probabilities enter the value product as two fp16 terms (21 bits).
  * Results do not depend on timing. workspace: device memory of
- * sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) bytes, 16-byte aligned, whose contents
+ * sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) bytes (at most 21 MB), 16-byte aligned, whose contents
  * need not be kept between calls; calls that can overlap need one each.
  */
 SAGE_API size_t sage_attn_kv4_workspace_size(int Hq, int Hkv, int max_q, int d);

@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
     uint8_t *ring = smem + warp * (C::kStages * C::kStageBytes);
     const uint32_t ring_at = smem_u32(ring) + lane * 16;
     const int ps = sq.page_size();
-    const int64_t page_bytes = kv4_page_bytes(ps, D), page_stride = sq.Hkv * page_bytes;
+    const int64_t page_bytes = kv4_page_bytes(ps, D);
+    const uint32_t page_stride = (uint32_t)(sq.Hkv * page_bytes);   // at most 65535 heads of 36864 bytes
     const int slice = min(ps, C::kTile);               // keys of a tile that one page holds
     const int slice_log2 = 31 - __clz(slice);
     // this lane's 16 bytes of a page's first rows (256 / D of a row's codes), and of its
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             }
             if (left >= C::kTile && slice == C::kTile) {       // a whole tile of one page
                 const int row = k0 & (ps - 1);
-                const uint8_t *src = head + __shfl_sync(0xffffffffu, ids, 0) * page_stride;
+                const uint8_t *src = head + (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, ids, 0) * page_stride;
                 const uint8_t *kc = src + row * (D / 2), *vc = kc + ps * (D / 2);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -481,16 +482,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 const int row0 = k0 & (ps - 1);                // not 0 only where slice == kTile
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int id = __shfl_sync(0xffffffffu, ids, i * kRowStep >> slice_log2);
-                    const uint8_t *kc = head + id * page_stride + (row0 + (i * kRowStep & (slice - 1))) * (D / 2);
+                    const uint32_t id = __shfl_sync(0xffffffffu, ids, i * kRowStep >> slice_log2);
+                    const uint8_t *kc = head + (uint64_t)id * page_stride + (row0 + (i * kRowStep & (slice - 1))) * (D / 2);
                     if (i * kRowStep + code_row < left) {
                         copy16(dst + i * 512, kc);
                         copy16(dst + C::kTile * (D / 2) + i * 512, kc + ps * (D / 2));
                     }
                 }
-                const int id = __shfl_sync(0xffffffffu, ids, par_row >> slice_log2);
+                const uint32_t id = __shfl_sync(0xffffffffu, ids, par_row >> slice_log2);
                 if (par_row < left)
-                    copy16(dst + C::kTile * D, head + id * page_stride + par_off +
+                    copy16(dst + C::kTile * D, head + (uint64_t)id * page_stride + par_off +
                                                    (row0 - (par_row & ~(slice - 1))) * (kG * 4));
             }
         }
@@ -1042,13 +1043,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv4_attn_merge(const Params 
     }
 }
 
-// What takes a call's rows per key head: the folded tile up to 4, one tile up to 8, else two.
-// Of the longest cache below, one row takes 252 us folded and 284 in a plain tile; 16 rows of 64
-// sequences take 147 us in two tiles and 175 in two passes of one.
+// What takes a call's rows per key head: the folded tile up to 4, else passes of one tile or of
+// two, whichever are the fewer at 1.68 times the cost. Of the longest cache below, one row takes
+// 252 us folded and 284 in a plain tile; of 64 ragged sequences, 16 rows take 147 us in one pass
+// of two tiles and 175 in two of one, 24 rows 268 in two of two and 249 in three of one.
 int variant(int Hq, int Hkv, int max_q)
 {
     const int rows = max_q * (Hq / Hkv);
-    return rows <= 4 ? 0 : rows <= 8 ? 1 : 2;
+    const int ones = (rows + 7) / 8, twos = (rows + 15) / 16;
+    return rows <= 4 ? 0 : 100 * ones >= 168 * twos ? 2 : 1;
 }
 int ctas(int var) { return (var < 2 ? 3 : 2) * kSMs; }
 int rows_of(int var) { return 4 << var; }
