@@ -80,7 +80,8 @@ struct Cfg {
     static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
     static constexpr int kPitch = D + 4;               // floats of a partial row: sums, reference, weight
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kSmem = kRing + kWarps * kRows * kPitch * 4;
+    static constexpr int kFloats = kTile * kGroups * 2;   // a tile's params in fp32, keys' or values'
+    static constexpr int kSmem = kRing + kWarps * (kRows * kPitch + 2 * kFloats) * 4;
 };
 
 // What a team that begins a (sequence, head, row block) and does not finish it leaves for the
@@ -136,16 +137,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 // -8 and -128 times 2^-24, twice: what centres the codes of the two kinds of channel.
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
 
-// (step, low) of a key's or value's groups.
+// A key's or value's two numbers for each of its groups, as the warp wrote them (below).
 template <int G>
-__device__ __forceinline__ void load_params(const uint32_t *at, float2 (&p)[G])
+__device__ __forceinline__ void load_params(const float *at, float2 (&p)[G])
 {
     if constexpr (G == 2) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(at);
-        p[0] = __half22float2(bits_h2(u.x));
-        p[1] = __half22float2(bits_h2(u.y));
+        const float4 u = *reinterpret_cast<const float4 *>(at);
+        p[0] = make_float2(u.x, u.y);
+        p[1] = make_float2(u.z, u.w);
     } else {
-        p[0] = __half22float2(bits_h2(*at));
+        p[0] = *reinterpret_cast<const float2 *>(at);
     }
 }
 
@@ -331,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
     __shared__ int s_seq[kWarps], s_segments;
     __shared__ Walk<D, NT, FOLD> s_walk[2 * kWarps];
     float *s_o = reinterpret_cast<float *>(smem + C::kRing);
+    float *kpar = s_o + kWarps * C::kRows * C::kPitch + threadIdx.x / 32 * (2 * C::kFloats);   // this warp's
+    float *vpar = kpar + C::kFloats;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const int cta = blockIdx.x;
@@ -588,14 +591,20 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
 
             // ---- scores, S^T: rows are keys, columns query rows; s f is the base-2 logit
             float s[kKB][NT][4];
-            const uint32_t *kpar = reinterpret_cast<const uint32_t *>(st + C::kTile * D);
+            // the keys' params to fp32, two groups a lane, for the four lanes that share a key
+            {
+                const uint2 u = reinterpret_cast<const uint2 *>(st + C::kTile * D)[lane];
+                const float2 x = __half22float2(bits_h2(u.x)), y = __half22float2(bits_h2(u.y));
+                reinterpret_cast<float4 *>(kpar)[lane] = make_float4(x.x, x.y, y.x, y.y);
+                __syncwarp();
+            }
 #pragma unroll
             for (int kb = 0; kb < kKB; kb++) {
                 const uint8_t *r0p = st + (kb * 16 + g) * (D / 2) + t4 * 8;
                 const uint8_t *r1p = r0p + 8 * (D / 2);
                 float2 p0[kG], p1[kG];
-                load_params<kG>(kpar + (kb * 16 + g) * kG, p0);
-                load_params<kG>(kpar + (kb * 16 + g + 8) * kG, p1);
+                load_params<kG>(kpar + (kb * 16 + g) * (2 * kG), p0);
+                load_params<kG>(kpar + (kb * 16 + g + 8) * (2 * kG), p1);
 #pragma unroll
                 for (int gr = 0; gr < kG; gr++) {
                     const uint2 w0 = *reinterpret_cast<const uint2 *>(r0p + gr * 32);
@@ -659,10 +668,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             // ---- the tile's largest value step: products p * step are scaled by a power of two
             // that keeps them below 2^15, whatever V's size. In a masked tile, rows behind the last
             // token and non-finite steps do not count (elsewhere every row sees every step)
-            const uint32_t *vpar = reinterpret_cast<const uint32_t *>(st + C::kTile * D + C::kParBytes);
-            uint2 vs = reinterpret_cast<const uint2 *>(vpar)[lane];
-            vs.x &= 0x7FFFu;
-            vs.y &= 0x7FFFu;
+            const uint2 vraw = reinterpret_cast<const uint2 *>(st + C::kTile * D + C::kParBytes)[lane];
+            uint2 vs = make_uint2(vraw.x & 0x7FFFu, vraw.y & 0x7FFFu);
             if (masked) {
                 if (vs.x >= 0x7C00u || k0 + 2 * lane / kG >= len)
                     vs.x = 0;
@@ -704,6 +711,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                     }
             }
 
+            // the values' params: step so scaled, and the middle low + 8 step
+            {
+                const float2 x = __half22float2(bits_h2(vraw.x)), y = __half22float2(bits_h2(vraw.y));
+                reinterpret_cast<float4 *>(vpar)[lane] =
+                    make_float4(x.x * vscale, fmaf(8.0f, x.x, x.y), y.x * vscale, fmaf(8.0f, y.x, y.y));
+                __syncwarp();
+            }
+
             // ---- probabilities and O^T += V^T P^T: rows are channels, columns query rows
             float centre[NT][kG][4];
 #pragma unroll
@@ -727,12 +742,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 }
                 const uint8_t *vr = st + (C::kTile + kb * 16 + 2 * t4) * (D / 2) + g * 4;
                 float2 p0[kG], p1[kG];
-                load_params<kG>(vpar + (kb * 16 + g) * kG, p0);
-                load_params<kG>(vpar + (kb * 16 + g + 8) * kG, p1);
+                load_params<kG>(vpar + (kb * 16 + g) * (2 * kG), p0);
+                load_params<kG>(vpar + (kb * 16 + g + 8) * (2 * kG), p1);
 #pragma unroll
                 for (int gr = 0; gr < kG; gr++) {
-                    const float step0 = p0[gr].x * vscale, step1 = p1[gr].x * vscale;
-                    const float mid0 = fmaf(8.0f, p0[gr].x, p0[gr].y), mid1 = fmaf(8.0f, p1[gr].x, p1[gr].y);
+                    const float step0 = p0[gr].x, step1 = p1[gr].x, mid0 = p0[gr].y, mid1 = p1[gr].y;
                     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
                     for (int i = 0; i < NT; i++) {
