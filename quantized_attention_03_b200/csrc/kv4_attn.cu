@@ -71,13 +71,13 @@ template <int D, int NT, bool FOLD>
 struct Cfg {
     static constexpr int kTile = 4096 / D;             // keys per warp tile
     static constexpr int kGroups = D / kKv4Group;
-    static constexpr int kStages = NT == 1 ? 2 : 3;
+    static constexpr int kStages = 2;                  // of 32 or 64 keys: 55 KB an SM in flight
     // 12 warps of 168 registers or 8 of 255; 16 of 128 registers spill: 98 against 86 us over the
     // ragged sequences below
     static constexpr int kCtasPerSM = NT == 1 ? 3 : 2;
     static constexpr int kRows = FOLD ? 4 : 8 * NT;
     static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
-    static constexpr int kStageBytes = kTile * D + 2 * kParBytes;
+    static constexpr int kStageBytes = kTile * D + 2 * kParBytes;   // 4608: the other stage is an XOR away
     static constexpr int kPitch = D + 4;               // floats of a partial row: sums, reference, weight
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kFloats = kTile * kGroups * 2;   // a tile's params in fp32, keys' or values'
@@ -499,9 +499,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        stage_in = C::kStages == 2                                     ? stage_in ^ C::kStageBytes
-                   : stage_in == (C::kStages - 1) * C::kStageBytes ? 0
-                                                                   : stage_in + C::kStageBytes;
+        stage_in ^= C::kStageBytes;
         next_tile += step;
         if (more)
             advance();
@@ -832,9 +830,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             else
                 tile(std::false_type{});
             __syncwarp();                              // the stage is read
-            stage_out = C::kStages == 2                                      ? stage_out ^ C::kStageBytes
-                        : stage_out == (C::kStages - 1) * C::kStageBytes ? 0
-                                                                         : stage_out + C::kStageBytes;
+            stage_out ^= C::kStageBytes;
             issue();
         }
 
