@@ -10,7 +10,7 @@
 // What bounds it: the cache is read once from HBM, 0.5625 bytes per element (B8 H32 over 32768
 // keys of d 128: 1.21 GB, 185 us at the copy bandwidth, which the copies alone reach), and each
 // element has to be turned from 4 bits into a 16-bit operand: the instructions are the bound,
-// 231 us for that cache without its copies, 250 us in all (4.8 TB/s).
+// 231 us for that cache without its copies, 245 us in all (4.9 TB/s).
 //   - A code masked in place is an fp16 subnormal, n 2^-24 or 16 n 2^-24, which the tensor core
 //     takes as it is; one AND makes two operands. The queries of the second kind of channel are
 //     divided by 16 beforehand, the outputs at the end. Sums of such products are good to 2^-18.
