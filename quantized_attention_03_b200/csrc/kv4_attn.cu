@@ -585,245 +585,249 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
             __syncwarp();                              // every lane's part has landed
             auto tile = [&](auto hides) {
-            constexpr bool masked = decltype(hides)::value;
+                constexpr bool masked = decltype(hides)::value;
 
-            // ---- scores, S^T: rows are keys, columns query rows; s f is the base-2 logit
-            float s[kKB][NT][4];
-            // the keys' params to fp32, two groups a lane, for the four lanes that share a key
-            {
-                const uint2 u = reinterpret_cast<const uint2 *>(st + C::kTile * D)[lane];
-                const float2 x = __half22float2(bits_h2(u.x)), y = __half22float2(bits_h2(u.y));
-                reinterpret_cast<float4 *>(kpar)[lane] = make_float4(x.x, x.y, y.x, y.y);
-                __syncwarp();
-            }
-#pragma unroll
-            for (int kb = 0; kb < kKB; kb++) {
-                const uint8_t *r0p = st + (kb * 16 + g) * (D / 2) + t4 * 8;
-                const uint8_t *r1p = r0p + 8 * (D / 2);
-                float2 p0[kG], p1[kG];
-                load_params<kG>(kpar + (kb * 16 + g) * (2 * kG), p0);
-                load_params<kG>(kpar + (kb * 16 + g + 8) * (2 * kG), p1);
-#pragma unroll
-                for (int gr = 0; gr < kG; gr++) {
-                    const uint2 w0 = *reinterpret_cast<const uint2 *>(r0p + gr * 32);
-                    const uint2 w1 = *reinterpret_cast<const uint2 *>(r1p + gr * 32);
-                    float acc[NT][4];
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        uint32_t u0 = j ? w0.y : w0.x, u1 = j ? w1.y : w1.x;
-#pragma unroll
-                        for (int hf = 0; hf < 2; hf++) {
-                            const uint32_t a0 = u0 & 0x000F000Fu, a1 = u1 & 0x000F000Fu;
-                            const uint32_t a2 = u0 & 0x00F000F0u, a3 = u1 & 0x00F000F0u;
-#pragma unroll
-                            for (int i = 0; i < NT; i++)
-                                if (j == 0 && hf == 0)
-                                    mma16816_first(acc[i], a0, a1, a2, a3, qf[i][gr][0][0], qf[i][gr][0][1]);
-                                else
-                                    mma16816(acc[i], a0, a1, a2, a3, qf[i][gr][j][2 * hf], qf[i][gr][j][2 * hf + 1]);
-                            u0 >>= 8;
-                            u1 >>= 8;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < NT; i++)
-#pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            const float2 pr = c < 2 ? p0[gr] : p1[gr];
-                            const float low = gr == 0 ? pr.y * qs[i][gr][c & 1] : fmaf(pr.y, qs[i][gr][c & 1], s[kb][i][c]);
-                            s[kb][i][c] = fmaf(pr.x, acc[i][c], low);
-                        }
+                // ---- scores, S^T: rows are keys, columns query rows; s f is the base-2 logit
+                float s[kKB][NT][4];
+                // the keys' params to fp32, two groups a lane, for the four lanes that share a key
+                {
+                    const uint2 u = reinterpret_cast<const uint2 *>(st + C::kTile * D)[lane];
+                    const float2 x = __half22float2(bits_h2(u.x)), y = __half22float2(bits_h2(u.y));
+                    reinterpret_cast<float4 *>(kpar)[lane] = make_float4(x.x, x.y, y.x, y.y);
+                    __syncwarp();
                 }
-            }
-            uint32_t hidden = 0;                       // of this lane's scores, bit kb*NT*4 + ...
-            if (masked) {
 #pragma unroll
-                for (int kb = 0; kb < kKB; kb++)
+                for (int kb = 0; kb < kKB; kb++) {
+                    const uint8_t *r0p = st + (kb * 16 + g) * (D / 2) + t4 * 8;
+                    const uint8_t *r1p = r0p + 8 * (D / 2);
+                    float2 p0[kG], p1[kG];
+                    load_params<kG>(kpar + (kb * 16 + g) * (2 * kG), p0);
+                    load_params<kG>(kpar + (kb * 16 + g + 8) * (2 * kG), p1);
 #pragma unroll
-                    for (int i = 0; i < NT; i++)
+                    for (int gr = 0; gr < kG; gr++) {
+                        const uint2 w0 = *reinterpret_cast<const uint2 *>(r0p + gr * 32);
+                        const uint2 w1 = *reinterpret_cast<const uint2 *>(r1p + gr * 32);
+                        float acc[NT][4];
 #pragma unroll
-                        for (int c = 0; c < 4; c++)
-                            if (k0 + kb * 16 + g + (c >> 1) * 8 > lim[i][c & 1]) {
-                                s[kb][i][c] = -INFINITY;
-                                hidden |= 1u << ((kb * NT + i) * 4 + c);
+                        for (int j = 0; j < 2; j++) {
+                            uint32_t u0 = j ? w0.y : w0.x, u1 = j ? w1.y : w1.x;
+#pragma unroll
+                            for (int hf = 0; hf < 2; hf++) {
+                                const uint32_t a0 = u0 & 0x000F000Fu, a1 = u1 & 0x000F000Fu;
+                                const uint32_t a2 = u0 & 0x00F000F0u, a3 = u1 & 0x00F000F0u;
+#pragma unroll
+                                for (int i = 0; i < NT; i++)
+                                    if (j == 0 && hf == 0)
+                                        mma16816_first(acc[i], a0, a1, a2, a3, qf[i][gr][0][0], qf[i][gr][0][1]);
+                                    else
+                                        mma16816(acc[i], a0, a1, a2, a3, qf[i][gr][j][2 * hf],
+                                                 qf[i][gr][j][2 * hf + 1]);
+                                u0 >>= 8;
+                                u1 >>= 8;
                             }
-            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT; i++)
+#pragma unroll
+                            for (int c = 0; c < 4; c++) {
+                                const float2 pr = c < 2 ? p0[gr] : p1[gr];
+                                const float sum = qs[i][gr][c & 1];
+                                const float low = gr == 0 ? pr.y * sum : fmaf(pr.y, sum, s[kb][i][c]);
+                                s[kb][i][c] = fmaf(pr.x, acc[i][c], low);
+                            }
+                    }
+                }
+                uint32_t hidden = 0;                       // of this lane's scores, bit kb*NT*4 + ...
+                if (masked) {
+#pragma unroll
+                    for (int kb = 0; kb < kKB; kb++)
+#pragma unroll
+                        for (int i = 0; i < NT; i++)
+#pragma unroll
+                            for (int c = 0; c < 4; c++)
+                                if (k0 + kb * 16 + g + (c >> 1) * 8 > lim[i][c & 1]) {
+                                    s[kb][i][c] = -INFINITY;
+                                    hidden |= 1u << ((kb * NT + i) * 4 + c);
+                                }
+                }
 
-            // ---- the reference m that probabilities are taken relative to moves only when a
-            // logit is more than 8 above it, so p <= 2^8
-            float x[NT][2];
-            bool move = false;
-#pragma unroll
-            for (int i = 0; i < NT; i++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    x[i][c] = fmaxf(s[0][i][c], s[0][i][c + 2]);
-#pragma unroll
-                    for (int kb = 1; kb < kKB; kb++)
-                        x[i][c] = fmaxf(x[i][c], fmaxf(s[kb][i][c], s[kb][i][c + 2]));
-                    move |= fmaf(x[i][c], f[i][c], nm[i][c]) > 8.0f;
-                }
-            // ---- the tile's largest value step: products p * step are scaled by a power of two
-            // that keeps them below 2^15, whatever V's size. In a masked tile, rows behind the last
-            // token and non-finite steps do not count (elsewhere every row sees every step)
-            const uint2 vraw = reinterpret_cast<const uint2 *>(st + C::kTile * D + C::kParBytes)[lane];
-            uint2 vs = make_uint2(vraw.x & 0x7FFFu, vraw.y & 0x7FFFu);
-            if (masked) {
-                if (vs.x >= 0x7C00u || k0 + 2 * lane / kG >= len)
-                    vs.x = 0;
-                if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= len)
-                    vs.y = 0;
-            }
-            const uint32_t vtop = max(vs.x, vs.y);
-            if (__any_sync(0xffffffffu, move || vtop >= vlimit)) {
-                const int texp = (int)(__reduce_max_sync(0xffffffffu, vtop) >> 10);
-                float shift = 1.0f;
-                if (texp > vexp + 3) {
-                    shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
-                    vexp = texp;
-                    vlimit = (uint32_t)(vexp + 4) << 10;
-                    vscale = __uint_as_float((uint32_t)(127 + 18 - vexp) << 23);
-                }
+                // ---- the reference m that probabilities are taken relative to moves only when a
+                // logit is more than 8 above it, so p <= 2^8
+                float x[NT][2];
+                bool move = false;
 #pragma unroll
                 for (int i = 0; i < NT; i++)
 #pragma unroll
                     for (int c = 0; c < 2; c++) {
-                        float y = x[i][c], alpha = 1.0f;
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) * f[i][c];
-                        if (y > -nm[i][c]) {           // (rows that have seen no key: -inf on both sides)
-                            alpha = ex2_approx(-nm[i][c] - y);
-                            nm[i][c] = -y;
-                        }
-                        l[i][c] *= alpha;
+                        x[i][c] = fmaxf(s[0][i][c], s[0][i][c + 2]);
 #pragma unroll
-                        for (int gr = 0; gr < kG; gr++) {
-                            o2[i][gr][c] *= alpha;
+                        for (int kb = 1; kb < kKB; kb++)
+                            x[i][c] = fmaxf(x[i][c], fmaxf(s[kb][i][c], s[kb][i][c + 2]));
+                        move |= fmaf(x[i][c], f[i][c], nm[i][c]) > 8.0f;
+                    }
+                // ---- the tile's largest value step: products p * step are scaled by a power of two
+                // that keeps them below 2^15, whatever V's size. In a masked tile, rows behind the last
+                // token and non-finite steps do not count (elsewhere every row sees every step)
+                const uint2 vraw = reinterpret_cast<const uint2 *>(st + C::kTile * D + C::kParBytes)[lane];
+                uint2 vs = make_uint2(vraw.x & 0x7FFFu, vraw.y & 0x7FFFu);
+                if (masked) {
+                    if (vs.x >= 0x7C00u || k0 + 2 * lane / kG >= len)
+                        vs.x = 0;
+                    if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= len)
+                        vs.y = 0;
+                }
+                const uint32_t vtop = max(vs.x, vs.y);
+                if (__any_sync(0xffffffffu, move || vtop >= vlimit)) {
+                    const int texp = (int)(__reduce_max_sync(0xffffffffu, vtop) >> 10);
+                    float shift = 1.0f;
+                    if (texp > vexp + 3) {
+                        shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
+                        vexp = texp;
+                        vlimit = (uint32_t)(vexp + 4) << 10;
+                        vscale = __uint_as_float((uint32_t)(127 + 18 - vexp) << 23);
+                    }
 #pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                o[i][gr][j][c] *= alpha * shift;
-                                o[i][gr][j][c + 2] *= alpha * shift;
+                    for (int i = 0; i < NT; i++)
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            float y = x[i][c], alpha = 1.0f;
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16)) * f[i][c];
+                            if (y > -nm[i][c]) {           // (rows that have seen no key: -inf on both sides)
+                                alpha = ex2_approx(-nm[i][c] - y);
+                                nm[i][c] = -y;
+                            }
+                            l[i][c] *= alpha;
+#pragma unroll
+                            for (int gr = 0; gr < kG; gr++) {
+                                o2[i][gr][c] *= alpha;
+#pragma unroll
+                                for (int j = 0; j < 4; j++) {
+                                    o[i][gr][j][c] *= alpha * shift;
+                                    o[i][gr][j][c + 2] *= alpha * shift;
+                                }
                             }
                         }
-                    }
-            }
-
-            // the values' params: step so scaled, and the middle low + 8 step
-            {
-                const float2 x = __half22float2(bits_h2(vraw.x)), y = __half22float2(bits_h2(vraw.y));
-                reinterpret_cast<float4 *>(vpar)[lane] =
-                    make_float4(x.x * vscale, fmaf(8.0f, x.x, x.y), y.x * vscale, fmaf(8.0f, y.x, y.y));
-                __syncwarp();
-            }
-
-            // ---- probabilities and O^T += V^T P^T: rows are channels, columns query rows
-            float centre[NT][kG][4];
-#pragma unroll
-            for (int kb = 0; kb < kKB; kb++) {
-#pragma unroll
-                for (int i = 0; i < NT; i++) {
-                    const float2 ff = make_float2(f[i][0], f[i][1]);
-                    // a row that has seen no key yet: 2^(-inf + 0)
-                    const float2 nn = make_float2(nm[i][0] == INFINITY ? 0.0f : nm[i][0],
-                                                  nm[i][1] == INFINITY ? 0.0f : nm[i][1]);
-                    const float2 ta = fma2(make_float2(s[kb][i][0], s[kb][i][1]), ff, nn);
-                    const float2 tb = fma2(make_float2(s[kb][i][2], s[kb][i][3]), ff, nn);
-                    s[kb][i][0] = ex2_approx(ta.x);
-                    s[kb][i][1] = ex2_approx(ta.y);
-                    s[kb][i][2] = ex2_approx(tb.x);
-                    s[kb][i][3] = ex2_approx(tb.y);
-                    const float2 ls = add2(make_float2(s[kb][i][0], s[kb][i][1]), make_float2(s[kb][i][2], s[kb][i][3]));
-                    const float2 lt = add2(make_float2(l[i][0], l[i][1]), ls);
-                    l[i][0] = lt.x;
-                    l[i][1] = lt.y;
                 }
-                const uint8_t *vr = st + (C::kTile + kb * 16 + 2 * t4) * (D / 2) + g * 4;
-                float2 p0[kG], p1[kG];
-                load_params<kG>(vpar + (kb * 16 + g) * (2 * kG), p0);
-                load_params<kG>(vpar + (kb * 16 + g + 8) * (2 * kG), p1);
+
+                // the values' params: step so scaled, and the middle low + 8 step
+                {
+                    const float2 x = __half22float2(bits_h2(vraw.x)), y = __half22float2(bits_h2(vraw.y));
+                    reinterpret_cast<float4 *>(vpar)[lane] =
+                        make_float4(x.x * vscale, fmaf(8.0f, x.x, x.y), y.x * vscale, fmaf(8.0f, y.x, y.y));
+                    __syncwarp();
+                }
+
+                // ---- probabilities and O^T += V^T P^T: rows are channels, columns query rows
+                float centre[NT][kG][4];
 #pragma unroll
-                for (int gr = 0; gr < kG; gr++) {
-                    const float step0 = p0[gr].x, step1 = p1[gr].x, mid0 = p0[gr].y, mid1 = p1[gr].y;
-                    uint32_t hi[NT][2], lo[NT][2];
+                for (int kb = 0; kb < kKB; kb++) {
 #pragma unroll
                     for (int i = 0; i < NT; i++) {
-                        float pv[4];
+                        const float2 ff = make_float2(f[i][0], f[i][1]);
+                        // a row that has seen no key yet: 2^(-inf + 0)
+                        const float2 nn = make_float2(nm[i][0] == INFINITY ? 0.0f : nm[i][0],
+                                                      nm[i][1] == INFINITY ? 0.0f : nm[i][1]);
+                        const float2 ta = fma2(make_float2(s[kb][i][0], s[kb][i][1]), ff, nn);
+                        const float2 tb = fma2(make_float2(s[kb][i][2], s[kb][i][3]), ff, nn);
+                        s[kb][i][0] = ex2_approx(ta.x);
+                        s[kb][i][1] = ex2_approx(ta.y);
+                        s[kb][i][2] = ex2_approx(tb.x);
+                        s[kb][i][3] = ex2_approx(tb.y);
+                        const float2 ls = add2(make_float2(s[kb][i][0], s[kb][i][1]),
+                                               make_float2(s[kb][i][2], s[kb][i][3]));
+                        const float2 lt = add2(make_float2(l[i][0], l[i][1]), ls);
+                        l[i][0] = lt.x;
+                        l[i][1] = lt.y;
+                    }
+                    const uint8_t *vr = st + (C::kTile + kb * 16 + 2 * t4) * (D / 2) + g * 4;
+                    float2 p0[kG], p1[kG];
+                    load_params<kG>(vpar + (kb * 16 + g) * (2 * kG), p0);
+                    load_params<kG>(vpar + (kb * 16 + g + 8) * (2 * kG), p1);
 #pragma unroll
-                        for (int c = 0; c < 4; c++)
-                            pv[c] = s[kb][i][c] * (c < 2 ? step0 : step1);
-                        if (masked) {                  // 0 times what lies in a hidden place is 0
+                    for (int gr = 0; gr < kG; gr++) {
+                        const float step0 = p0[gr].x, step1 = p1[gr].x, mid0 = p0[gr].y, mid1 = p1[gr].y;
+                        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-                            for (int c = 0; c < 4; c++) {
-                                const bool hid = hidden >> ((kb * NT + i) * 4 + c) & 1;
-                                pv[c] = hid ? 0.0f : pv[c];
-                                o2[i][gr][c & 1] = hid ? o2[i][gr][c & 1]
-                                                       : fmaf(s[kb][i][c], c < 2 ? mid0 : mid1, o2[i][gr][c & 1]);
-                            }
-                        } else {
+                        for (int i = 0; i < NT; i++) {
+                            float pv[4];
 #pragma unroll
                             for (int c = 0; c < 4; c++)
-                                o2[i][gr][c & 1] = fmaf(s[kb][i][c], c < 2 ? mid0 : mid1, o2[i][gr][c & 1]);
-                        }
+                                pv[c] = s[kb][i][c] * (c < 2 ? step0 : step1);
+                            if (masked) {                  // 0 times what lies in a hidden place is 0
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const float2 v = make_float2(pv[2 * h], pv[2 * h + 1]);
-                            const __half2 a = __floats2half2_rn(v.x, v.y);
-                            // FOLD: this lane's columns take the high term (0) or the low one (-1)
-                            const float2 d = fma2(__half22float2(a), FOLD ? low_sel : make_float2(-1.0f, -1.0f), v);
-                            hi[i][h] = transpose8x8(FOLD ? pack_half2(d.x, d.y) : h2_bits(a));
-                            if (!FOLD)
-                                lo[i][h] = transpose8x8(pack_half2(d.x, d.y));
-                        }
-                    }
-                    // keys 2t, 2t+1 (A, B) and 2t+8, 2t+9 (C, D) of the block; 8 channels each
-                    const uint32_t wa = *reinterpret_cast<const uint32_t *>(vr + gr * 32);
-                    const uint32_t wb = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + D / 2);
-                    const uint32_t wc = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 8 * (D / 2));
-                    const uint32_t wd = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 9 * (D / 2));
-                    // minus 8 (and 128) for every code of the block, into sums of their own
+                                for (int c = 0; c < 4; c++) {
+                                    const bool hid = hidden >> ((kb * NT + i) * 4 + c) & 1;
+                                    pv[c] = hid ? 0.0f : pv[c];
+                                    o2[i][gr][c & 1] = hid ? o2[i][gr][c & 1]
+                                                           : fmaf(s[kb][i][c], c < 2 ? mid0 : mid1, o2[i][gr][c & 1]);
+                                }
+                            } else {
 #pragma unroll
-                    for (int i = 0; i < NT; i++) {
-                        if (kb == 0)
-                            mma16816_first(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, hi[i][0], hi[i][1]);
-                        else
-                            mma16816(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, hi[i][0], hi[i][1]);
-                        if (!FOLD)
-                            mma16816(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, lo[i][0], lo[i][1]);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; q++) {      // channels 0-3, then 4-7 of the word
-                        uint32_t ab = __byte_perm(wa, wb, q ? 0x7632 : 0x5410);
-                        uint32_t cd = __byte_perm(wc, wd, q ? 0x7632 : 0x5410);
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const uint32_t a0 = ab & 0x000F000Fu, a1 = ab & 0x00F000F0u;
-                            const uint32_t a2 = cd & 0x000F000Fu, a3 = cd & 0x00F000F0u;
-#pragma unroll
-                            for (int i = 0; i < NT; i++) {
-                                mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, hi[i][0], hi[i][1]);
-                                if (!FOLD)
-                                    mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, lo[i][0], lo[i][1]);
+                                for (int c = 0; c < 4; c++)
+                                    o2[i][gr][c & 1] = fmaf(s[kb][i][c], c < 2 ? mid0 : mid1, o2[i][gr][c & 1]);
                             }
-                            ab >>= 8;
-                            cd >>= 8;
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const float2 v = make_float2(pv[2 * h], pv[2 * h + 1]);
+                                const __half2 a = __floats2half2_rn(v.x, v.y);
+                                // FOLD: this lane's columns take the high term (0) or the low one (-1)
+                                const float2 d = fma2(__half22float2(a), FOLD ? low_sel : make_float2(-1.0f, -1.0f), v);
+                                hi[i][h] = transpose8x8(FOLD ? pack_half2(d.x, d.y) : h2_bits(a));
+                                if (!FOLD)
+                                    lo[i][h] = transpose8x8(pack_half2(d.x, d.y));
+                            }
+                        }
+                        // keys 2t, 2t+1 (A, B) and 2t+8, 2t+9 (C, D) of the block; 8 channels each
+                        const uint32_t wa = *reinterpret_cast<const uint32_t *>(vr + gr * 32);
+                        const uint32_t wb = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + D / 2);
+                        const uint32_t wc = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 8 * (D / 2));
+                        const uint32_t wd = *reinterpret_cast<const uint32_t *>(vr + gr * 32 + 9 * (D / 2));
+                        // minus 8 (and 128) for every code of the block, into sums of their own
+#pragma unroll
+                        for (int i = 0; i < NT; i++) {
+                            if (kb == 0)
+                                mma16816_first(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, hi[i][0],
+                                               hi[i][1]);
+                            else
+                                mma16816(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, hi[i][0], hi[i][1]);
+                            if (!FOLD)
+                                mma16816(centre[i][gr], kMinus8, kMinus128, kMinus8, kMinus128, lo[i][0], lo[i][1]);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {      // channels 0-3, then 4-7 of the word
+                            uint32_t ab = __byte_perm(wa, wb, q ? 0x7632 : 0x5410);
+                            uint32_t cd = __byte_perm(wc, wd, q ? 0x7632 : 0x5410);
+#pragma unroll
+                            for (int e = 0; e < 2; e++) {
+                                const uint32_t a0 = ab & 0x000F000Fu, a1 = ab & 0x00F000F0u;
+                                const uint32_t a2 = cd & 0x000F000Fu, a3 = cd & 0x00F000F0u;
+#pragma unroll
+                                for (int i = 0; i < NT; i++) {
+                                    mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, hi[i][0], hi[i][1]);
+                                    if (!FOLD)
+                                        mma16816(o[i][gr][2 * q + e], a0, a1, a2, a3, lo[i][0], lo[i][1]);
+                                }
+                                ab >>= 8;
+                                cd >>= 8;
+                            }
                         }
                     }
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < NT; i++)
+                for (int i = 0; i < NT; i++)
 #pragma unroll
-                for (int gr = 0; gr < kG; gr++)
+                    for (int gr = 0; gr < kG; gr++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
+                        for (int j = 0; j < 4; j++)
 #pragma unroll
-                        for (int c = 0; c < 4; c += 2) {
-                            const float2 y = add2(make_float2(o[i][gr][j][c], o[i][gr][j][c + 1]),
-                                                  make_float2(centre[i][gr][c], centre[i][gr][c + 1]));
-                            o[i][gr][j][c] = y.x;
-                            o[i][gr][j][c + 1] = y.y;
-                        }
+                            for (int c = 0; c < 4; c += 2) {
+                                const float2 y = add2(make_float2(o[i][gr][j][c], o[i][gr][j][c + 1]),
+                                                      make_float2(centre[i][gr][c], centre[i][gr][c + 1]));
+                                o[i][gr][j][c] = y.x;
+                                o[i][gr][j][c + 1] = y.y;
+                            }
             };
             if (k0 + C::kTile - 1 > seen)
                 tile(std::true_type{});
