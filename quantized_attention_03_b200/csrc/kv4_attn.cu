@@ -543,8 +543,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 qs[i][gr][0] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8);
                 qs[i][gr][1] = __shfl_sync(0xffffffffu, sum[gr], t4 * 8 + 4);
             }
-            f[i][0] = __shfl_sync(0xffffffffu, f[i][0], t4 * 8) * p.sc_log2;
-            f[i][1] = __shfl_sync(0xffffffffu, f[i][1], t4 * 8 + 4) * p.sc_log2;
+            // not 0, however small the row and the scale: a hidden score, -inf, times 0 is NaN
+            const float least = __uint_as_float(1u << 23);
+            f[i][0] = fmaxf(__shfl_sync(0xffffffffu, f[i][0], t4 * 8) * p.sc_log2, least);
+            f[i][1] = fmaxf(__shfl_sync(0xffffffffu, f[i][1], t4 * 8 + 4) * p.sc_log2, least);
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 const int rr = FOLD ? (2 * t4 + c) % 4 : i * 8 + 2 * t4 + c;

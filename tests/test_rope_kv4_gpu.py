@@ -436,6 +436,21 @@ def test_hidden_places_do_not_reach_the_result():
     assert out[4].isfinite().all()
 
 
+@pytest.mark.parametrize("Hq", [2, 4, 16, 32])
+def test_zero_queries_at_a_scale_that_underflows(Hq):
+    # logits of 0 over the keys that a query sees, and none over the hidden ones: every visible
+    # key counts alike
+    w = World([70, 3, 20], [4, 5, 1], 2, 128, 16, seed=16)
+    w.fill()
+    q = torch.randn((w.total, Hq, 128), generator=w.g).to(F16)
+    q[:3] = 0.0
+    q[6] = 0.0
+    lse = torch.empty((w.total, Hq), device="cuda")
+    out = sage.attn_kv4(q.cuda(), w.cache.cuda(), *w.where(), 5, sm_scale=1e-30, lse=lse)
+    ok()
+    check_attn(w, q, out, lse, sm_scale=1e-30)
+
+
 def test_non_finite_inputs_stay_in_their_group():
     w = World([20], [20], 2, 128, 32)
     k = torch.randn((20, 2, 128), generator=w.g).to(F16)
