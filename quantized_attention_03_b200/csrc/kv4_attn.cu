@@ -244,7 +244,7 @@ __device__ __forceinline__ int sequence(const Params &p, int s, int &row0, int &
         atomicOr(p.a.s.status, status_bit(SAGE_ERR_BAD_SEQLENS));
         return 0;
     }
-    nt = max(1, (len + C::kTile - 1) / C::kTile);
+    nt = max(1, (int)(((uint32_t)len + C::kTile - 1) / C::kTile));   // (len may be 2^31 - 1)
     nrb = (n * p.group + C::kRows - 1) / C::kRows;
     return nrb * p.a.s.Hkv;
 }

@@ -670,3 +670,22 @@ def test_pages_past_four_gigabytes():
     near(vo, vv, 2.0 ** -24 * vv.abs())
     want, _, _, _ = ref.attend(q.double(), kk, vv)
     near(out, want, 2.0 ** -13 * vv.abs().amax())
+
+
+def test_the_longest_sequence():
+    # 2^31 - 1 tokens, all on one page: equal weights over values of which the first 64 of 256
+    # are 0 and the others 1. A lane adds 2^31 / (1776 warps 8 lanes) = 151 000 terms, each sum
+    # off by at most 2^-24 of itself a term; two such sums make the result
+    w = World([256], [1], 1, 64, 256)
+    v = (torch.arange(256) >= 64).float()[:, None, None].expand(256, 1, 64)
+    w.put(0, torch.arange(256), torch.zeros(256, 1, 64), v)
+    n = 2 ** 31 - 1
+    table = torch.full((1, 2 ** 23), int(w.table[0, 0]), dtype=torch.int32, device="cuda")
+    kv_lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 1, 64), generator=w.g).to(F16).cuda()
+    out = sage.attn_kv4(q, w.cache.cuda(), table, kv_lens)
+    _, last = sage.kv4_gather(w.cache.cuda(), table, kv_lens, None, 1, 64)
+    ok()
+    assert (last == 1).all()
+    want = torch.full((1, 1, 64), 1 - 64 * 2 ** 23 / n, dtype=torch.float64)
+    near(out, want, 2 * 151_000 * 2.0 ** -24)
