@@ -688,7 +688,8 @@ def attn_kv4(q, cache, block_table, kv_lens, cu_seqlens=None, max_q: Optional[in
     """Attention of q [T, Hq, d] (any token and head strides) over the paged 4-bit cache; query
     head h reads key head h // (Hq / Hkv). A sequence has at most max_q queries (by default T /
     nseq without cu_seqlens, else DECODE_MAX_Q), which are its last tokens. lse: float32 [T, Hq]
-    that takes the log of the softmax sums. The workspace is allocated here unless given."""
+    that takes the log of the softmax sums. The workspace is allocated here unless given; what is
+    allocated belongs to the stream that the call runs on."""
     return _done("sage_attn_kv4", (_calls or _bound()).attn_kv4(
         q, cache, block_table, kv_lens, cu_seqlens, max_q, causal, sm_scale, out, lse, workspace,
         None if stream is None else _stream(stream)))

@@ -104,21 +104,34 @@ int to32(int64_t x, const Tensor &t, const char *what)
     return (int)x;
 }
 
-// The device of the call's tensors made current, and the stream: the one given (a pointer), or
-// torch's current one of that device.
+// The device of the call's tensors and the stream given (a pointer) made current, so that what
+// the call allocates belongs to the stream that uses it: a workspace is free again when the call
+// returns, and only that stream's order keeps the kernel's use before the next one's.
 struct Where {
-    std::optional<c10::cuda::CUDAGuard> guard;
-    sage_stream_t stream = nullptr;
+    const Tensor &x;
+    std::optional<c10::cuda::CUDAGuard> device;
+    std::optional<c10::cuda::CUDAStreamGuard> on;
+    sage_stream_t given = nullptr;
 
-    Where(const Tensor &x, const Args &a, int stream_arg)
+    Where(const Tensor &x, const Args &a, int stream_arg) : x(x)
+    {
+        if (!x.is_cuda())
+            return;
+        if (x.get_device() != c10::cuda::current_device())
+            device.emplace(x.device());
+        if (a.none(stream_arg))
+            return;
+        const uintptr_t raw = (uintptr_t)a.integer(stream_arg);
+        given = reinterpret_cast<sage_stream_t>(raw);
+        on.emplace(raw <= 1 ? c10::cuda::getDefaultCUDAStream(x.get_device())    // 0, cudaStreamLegacy
+                            : c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(raw), x.get_device()));
+    }
+    sage_stream_t stream() const
     {
         want(x.is_cuda(), x, "the tensors are on a CUDA device");
-        if (x.get_device() != c10::cuda::current_device())
-            guard.emplace(x.device());
-        if (a.none(stream_arg))
-            stream = reinterpret_cast<sage_stream_t>(c10::cuda::getCurrentCUDAStream(x.get_device()).stream());
-        else
-            stream = reinterpret_cast<sage_stream_t>((uintptr_t)a.integer(stream_arg));
+        if (on)
+            return given;
+        return reinterpret_cast<sage_stream_t>(c10::cuda::getCurrentCUDAStream(x.get_device()).stream());
     }
 };
 
@@ -150,6 +163,7 @@ PyObject *rope(const Args &a)
         s[at + 1] = x.stride(1);
         s[at + 2] = x.stride(packed ? 0 : 2);
     };
+    const Where w(q, a, 9);
     Tensor q_out = a.none(7) ? at::empty_like(q) : a.tensor(7, "q_out"), k_out;
     want(q_out.sizes() == q.sizes() && same(q_out, q) && q_out.stride(-1) == 1, q_out,
          "q_out has q's shape, type and device");
@@ -181,13 +195,12 @@ PyObject *rope(const Args &a)
         positions = static_cast<const int32_t *>(p.const_data_ptr());
         pos_stride = two ? p.stride(0) : 0;
     }
-    const Where w(q, a, 9);
     const sage_status_t rc = p_rope(
         q.const_data_ptr(), q_out.mutable_data_ptr(), has_k ? k->const_data_ptr() : nullptr,
         has_k ? k_out.mutable_data_ptr() : nullptr, positions, freqs, type, to32(B, q, "q has too many sequences"),
         to32(N, q, "q has too many tokens"), to32(q.size(1), q, "q has too many heads"),
         has_k ? to32(k->size(1), *k, "k has too many heads") : 0, to32(d, q, "q's head dim is too large"), rot, pos_stride,
-        s, a.real(4), (a.truth(5) ? SAGE_ROPE_INTERLEAVED : 0) | (a.truth(6) ? SAGE_ROPE_INVERSE : 0), w.stream);
+        s, a.real(4), (a.truth(5) ? SAGE_ROPE_INTERLEAVED : 0) | (a.truth(6) ? SAGE_ROPE_INVERSE : 0), w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
     PyObject *qo = THPVariable_Wrap(std::move(q_out));
@@ -241,6 +254,7 @@ PyObject *append(const Args &a)
     want(k.size(1) == s.Hkv && k.stride(2) == 1 && k.device() == s.cache.device(), k,
          "k is [T, Hkv, d] with the cache's heads and device, its channels contiguous");
     want(v.sizes() == k.sizes() && same(v, k) && v.stride(2) == 1, v, "v has k's shape, type and device");
+    const Where w(k, a, 12);
     int64_t st[8] = {k.stride(0), k.stride(1), v.stride(0), v.stride(1), 0, 0, 0, 0};
     const Tensor *q = nullptr;
     Tensor q_out;
@@ -266,13 +280,12 @@ PyObject *append(const Args &a)
              "k_mean is a contiguous float32 [Hkv, d] on the cache's device");
         mean = static_cast<const float *>(m.const_data_ptr());
     }
-    const Where w(k, a, 12);
     const sage_status_t rc = p_append(
         s.cache.mutable_data_ptr(), s.table_at(), s.lens_at(), s.cu, k.const_data_ptr(), v.const_data_ptr(),
         q ? q->const_data_ptr() : nullptr, q ? q_out.mutable_data_ptr() : nullptr, freqs, mean, type, s.nseq,
         to32(k.size(0), k, "k has too many tokens"), q ? to32(q->size(1), *q, "q has too many heads") : 0, s.Hkv,
         (int)k.size(2), s.page_size, s.num_pages, s.max_pages, rot, st, a.real(8),
-        a.truth(9) ? SAGE_ROPE_INTERLEAVED : 0, w.stream);
+        a.truth(9) ? SAGE_ROPE_INTERLEAVED : 0, w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
     return q ? THPVariable_Wrap(std::move(q_out)) : Py_NewRef(Py_None);
@@ -286,6 +299,7 @@ PyObject *gather(const Args &a)
     const Seqs s(a, 0, d);
     if (total < 0 || rep < 1)
         throw Refused("total is not negative and rep is at least 1");
+    const Where w(s.cache, a, 10);
     const int64_t shape[3] = {total, (int64_t)s.Hkv * rep, d};
     auto out = [&](int i, const char *name) -> Tensor {
         if (a.none(i))
@@ -297,10 +311,9 @@ PyObject *gather(const Args &a)
         return x;
     };
     Tensor k = out(8, "k_out"), v = out(9, "v_out");
-    const Where w(s.cache, a, 10);
     const sage_status_t rc = p_gather(s.cache.const_data_ptr(), s.table_at(), s.lens_at(), s.cu, k.mutable_data_ptr(),
                                       v.mutable_data_ptr(), type == at::kHalf ? SAGE_F16 : SAGE_BF16, s.nseq, total,
-                                      s.Hkv, rep, d, s.page_size, s.num_pages, s.max_pages, w.stream);
+                                      s.Hkv, rep, d, s.page_size, s.num_pages, s.max_pages, w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
     PyObject *ko = THPVariable_Wrap(std::move(k)), *vo = THPVariable_Wrap(std::move(v));
@@ -316,6 +329,7 @@ PyObject *attn(const Args &a)
     const Seqs s(a, 1, q.size(2));
     want(q.device() == s.cache.device() && q.stride(2) == 1, q,
          "q is [T, Hq, d] on the cache's device, its channels contiguous");
+    const Where w(q, a, 11);
     Tensor out = a.none(8) ? at::empty(q.sizes(), q.options()) : a.tensor(8, "out");
     want(out.sizes() == q.sizes() && same(out, q) && out.is_contiguous(), out,
          "out is contiguous and has q's shape, type and device");
@@ -337,11 +351,10 @@ PyObject *attn(const Args &a)
         want(ws.is_contiguous() && ws.device() == q.device(), ws, "workspace is contiguous and on q's device");
     }
     const int64_t st[2] = {q.stride(0), q.stride(1)};
-    const Where w(q, a, 11);
     const sage_status_t rc =
         p_attn(q.const_data_ptr(), s.cache.const_data_ptr(), s.table_at(), s.lens_at(), s.cu, out.mutable_data_ptr(), lse,
                type, s.nseq, T, max_q, Hq, s.Hkv, (int)q.size(2), s.page_size, s.num_pages, s.max_pages, a.truth(6),
-               (float)a.real(7), st, ws.mutable_data_ptr(), ws.nbytes(), w.stream);
+               (float)a.real(7), st, ws.mutable_data_ptr(), ws.nbytes(), w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
     return THPVariable_Wrap(std::move(out));

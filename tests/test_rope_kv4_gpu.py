@@ -493,6 +493,36 @@ def test_same_bits_again_and_on_another_stream():
     ok()
 
 
+def test_what_a_call_allocates_belongs_to_its_stream():
+    # a workspace is free again when the call returns: memory of another stream could be handed
+    # out to that stream while the kernel still uses it
+    def owner(ptr):
+        return [x["stream"] for x in torch.cuda.memory_snapshot()
+                if x["address"] <= ptr < x["address"] + x["total_size"]]
+
+    w = World([500, 40], [1, 1], 2, 64, 16, seed=17)
+    w.fill()
+    q, kv = (torch.randn((2, h, 64), generator=w.g).to(F16).cuda() for h in (4, 2))
+    cache, spare, where = w.cache.cuda(), w.cache.cuda(), w.where()
+    freqs = torch.tensor([2.0 ** -i for i in range(32)], dtype=torch.float64).cuda()
+    want = sage.attn_kv4(q, cache, *where, 1)
+    torch.cuda.synchronize()
+    for s in (torch.cuda.Stream(), torch.cuda.default_stream()):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [*sage.rope(q, kv, freqs=freqs, stream=s), sage.attn_kv4(q, cache, *where, 1, stream=s),
+                   *sage.kv4_gather(cache, *where, 2, 64, stream=s),
+                   sage.kv4_append(spare, *where, kv, kv, q=q, freqs=freqs, stream=s)]
+            assert all(owner(x.data_ptr()) == [s.cuda_stream] for x in got)
+            s.synchronize()
+            assert torch.equal(got[2].cpu(), want.cpu())
+            t = torch.cuda.Stream(priority=-1)         # for the workspace alone
+            sage.attn_kv4(q, cache, *where, 1, out=got[2], stream=t)
+            need = sage.sage_attn_kv4_workspace_size(4, 2, 1, 64)
+            assert sum(x["total_size"] for x in torch.cuda.memory_snapshot() if x["stream"] == t.cuda_stream) >= need
+            t.synchronize()
+    ok()
+
+
 def test_a_serving_loop_in_a_graph():
     """Prompt by append, gather and the package's own prefill attention; then decode steps,
     each an append and an attention captured once and replayed with new lengths."""
