@@ -426,7 +426,7 @@ SAGE_API sage_status_t sage_kv4_append(void *cache, const int32_t *block_table,
 
 /*
  * Gather: the last tokens of every sequence as k_out and v_out [total, Hkv*rep, d], each head
- * written rep times side by side (for attention entry points that take as many key heads as
+ * written rep times side by side, Hkv*rep at most 65535 (for attention entry points that take as many key heads as
  * query heads). With cu_seqlens the running sum of kv_lens: all of them. Allocates nothing.
  */
 SAGE_API sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_table,

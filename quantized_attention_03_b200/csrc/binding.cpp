@@ -299,6 +299,8 @@ PyObject *gather(const Args &a)
     const Seqs s(a, 0, d);
     if (total < 0 || rep < 1)
         throw Refused("total is not negative and rep is at least 1");
+    if ((int64_t)s.Hkv * rep > 65535)                  // before outputs of that size are asked for
+        return PyLong_FromLong(SAGE_ERR_UNSUPPORTED);
     const Where w(s.cache, a, 10);
     const int64_t shape[3] = {total, (int64_t)s.Hkv * rep, d};
     auto out = [&](int i, const char *name) -> Tensor {

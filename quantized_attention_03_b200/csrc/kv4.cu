@@ -421,7 +421,7 @@ cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, cudaStream_t st)
 {
     // tokens of a CTA: about 2048 stores of 16 bytes, but at least 2 CTAs an SM. 16384 tokens of 8
     // heads, each written 4 times: 48 us with 2 tokens, 51 with 8; once: 26 and 20
-    const int stores = a.s.Hkv * (a.d / 8) * a.rep * 2;
+    const int stores = a.s.Hkv * (a.d / 8) * a.rep * 2;   // Hkv rep is at most 65535
     const int tpc = std::max(1, std::min({kMaxTokens, std::max(2, 2048 / stores), a.s.total / 592}));
     const int grid = (a.s.total + tpc - 1) / tpc;
     auto go = [&](auto kern) { return launch_overlapped(kern, dim3(grid), kThreads, 0, st, a, tpc); };

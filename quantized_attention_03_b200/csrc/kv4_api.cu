@@ -196,6 +196,8 @@ sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_table,
         return r;
     if (rep < 1)
         return SAGE_ERR_INVALID_ARG;
+    if ((int64_t)Hkv * rep > 65535)
+        return SAGE_ERR_UNSUPPORTED;
     if (nseq == 0 || total == 0 || Hkv == 0)
         return SAGE_OK;
     if (!cache || !block_table || !kv_lens || !k_out || !v_out)

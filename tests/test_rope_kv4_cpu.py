@@ -136,6 +136,16 @@ def test_gather_refusals(lib):
     assert _gather(lib, total=0, ko=0) == sage.SAGE_OK
 
 
+@pytest.mark.parametrize("Hkv,rep", [(8, 1 << 24), (2, 1 << 30), (1, 65536), (65535, 2), (4, 2 ** 31 - 1)])
+def test_gather_refuses_more_heads_than_the_other_calls(lib, Hkv, rep):
+    # heads of the outputs, as everywhere at most 65535: products of them stay within 32 bits
+    assert _gather(lib, Hkv=Hkv, rep=rep) == sage.SAGE_ERR_UNSUPPORTED
+    assert _gather(lib, Hkv=Hkv, rep=rep, total=0) == sage.SAGE_ERR_UNSUPPORTED
+    cache, table, lens, cu = _cpu_sequences(Hkv=min(Hkv, 8))
+    with pytest.raises(sage.SageError):
+        sage.kv4_gather(cache, table, lens, cu, 2, 64, rep=max(rep, 65536))
+
+
 def _attn(lib, q=FAKE, cache=FAKE, table=FAKE, lens=FAKE, cu=FAKE, out=FAKE, lse=None, dtype=0, nseq=2, total=4,
           max_q=2, Hq=4, Hkv=2, d=128, page=16, pages=8, width=4, strides=None, ws=FAKE, ws_bytes=1 << 30):
     s = None if strides is None else (ctypes.c_int64 * 2)(*strides)
