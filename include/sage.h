@@ -370,8 +370,9 @@ SAGE_API sage_status_t sage_rope_freqs(double *freqs, double *mscale, int rot_di
  * device, [B,N] with pos_stride elements between batches, 0 for [N] shared by all; NULL:
  * 0 .. N-1). strides: {batch, head, token} of q, q_out, k, k_out (12 values), or NULL for
  * dense tensors. Packed [T,H,d] tensors are B = 1, N = T with strides {0, d, H*d}. k may be
- * NULL (Hk = 0). q_out = q with the same strides rotates in place; other overlaps are not
- * allowed. freqs: double [rot_dim/2] on the device. flags: SAGE_ROPE_INTERLEAVED |
+ * NULL (Hk = 0). q_out = q with the same strides rotates in place (other strides are
+ * SAGE_ERR_INVALID_ARG, as is an output stride of 0 over several places); other overlaps are
+ * not allowed. freqs: double [rot_dim/2] on the device. flags: SAGE_ROPE_INTERLEAVED |
  * SAGE_ROPE_INVERSE. Allocates nothing.
  */
 SAGE_API sage_status_t sage_rope(const void *q, void *q_out, const void *k, void *k_out,
@@ -412,8 +413,9 @@ SAGE_API size_t sage_kv4_page_bytes(int page_size, int d);
  * not change when every key of a head is moved by the same vector, and a key's 4-bit range is
  * not spent on a channel offset (the smoothing of step 1 for a cache that grows). q
  * [total,Hq,d] is rotated to q_out alike, or NULL. strides: {token, head} of k, v, q, q_out
- * (8 values), or NULL for contiguous tensors. q_out may be q with the same strides. The pages
- * of a call's new tokens must belong to one sequence each. Allocates nothing.
+ * (8 values), or NULL for contiguous tensors. q_out may be q with the same strides (as
+ * sage_rope's) and overlaps nothing else. The pages of a call's new tokens must belong to one
+ * sequence each. Allocates nothing.
  */
 SAGE_API sage_status_t sage_kv4_append(void *cache, const int32_t *block_table,
                                        const int32_t *kv_lens, const int32_t *cu_seqlens,
@@ -439,8 +441,8 @@ SAGE_API sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_t
  * Attention of q [total,Hq,d] (strides q_strides {token, head}, NULL: contiguous) over the
  * cache: query head h reads key head h / (Hq/Hkv). A sequence has at most max_q <=
  * SAGE_DECODE_MAX_Q queries; its query i of n sees keys j <= kv_len - n + i (causal) or all
- * of them. out [total,Hq,d]; lse (fp32 [total,Hq], natural log of the sum of exp, or NULL).
- * A query that sees no key gets zeros and -inf. sm_scale <= 0 selects 1/sqrt(d). Scores and
+ * of them. out [total,Hq,d] may be q where that is contiguous, and overlaps nothing else; lse
+ * (fp32 [total,Hq], natural log of the sum of exp, or NULL). A query that sees no key gets zeros and -inf. sm_scale <= 0 selects 1/sqrt(d). Scores and
  * softmax are fp32; probabilities enter the value product as two fp16 terms (21 bits).
  * Results do not depend on timing. workspace: device memory of
  * sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) bytes (at most 21 MB), 16-byte aligned, whose contents

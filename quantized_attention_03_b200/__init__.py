@@ -640,7 +640,8 @@ def rope(q, k, freqs, positions=None, mscale: float = 1.0, interleaved: bool = F
     """Rotary positions of q [B, Hq, N, d] and k [B, Hk, N, d], or packed [T, H, d] (any
     strides; k may be None): (q_out, k_out). freqs and mscale: rope_freqs. positions int32 [N],
     [B, N] or [T]; None: 0 .. N-1. interleaved: pairs (2i, 2i+1), else (i, i + rot/2). inverse:
-    the rotation back, which is also its gradient. q_out=q, k_out=k rotates in place."""
+    the rotation back, which is also its gradient. q_out=q, k_out=k rotates in place; outputs
+    that overlap inputs or each other otherwise raise ValueError where that can be seen."""
     return _done("sage_rope", (_calls or _bound()).rope(
         q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out,
         None if stream is None else _stream(stream)))

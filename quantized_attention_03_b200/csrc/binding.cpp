@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -104,6 +105,92 @@ int to32(int64_t x, const Tensor &t, const char *what)
     return (int)x;
 }
 
+// Outputs that the caller gives. Kernels write an output while they read inputs and write other
+// outputs, so its elements lie apart from each other and from those, but that an output may be
+// its input itself (same address, same strides), where each element is read before it is written.
+
+// A dimension with more than one place, its step in elements.
+struct Dim {
+    int64_t step, a, b;                                // sizes in two tensors of the same steps
+};
+
+// Whether some difference of two places, i in (-d.b, d.a) along each of n dimensions, is `at`
+// elements. Steps ascend and each is at least the extent of those before it, so that at most two
+// i of a dimension leave a rest within their reach.
+bool reaches(const Dim *d, int n, int64_t at)
+{
+    if (n == 0)
+        return at == 0;
+    const Dim &x = d[n - 1];
+    const int64_t i = at >= 0 ? at / x.step : -((-at + x.step - 1) / x.step);      // floor
+    for (int64_t j = i; j <= i + 1; j++)
+        if (j > -x.b && j < x.a && reaches(d, n - 1, at - j * x.step))
+            return true;
+    return false;
+}
+
+// Dimensions of x and y (y with other sizes but the same steps, else x twice) by ascending step;
+// -1 where steps differ, -2 where places of one tensor can coincide.
+int dims_of(const Tensor &x, const Tensor &y, Dim (&d)[4])
+{
+    int n = 0;
+    for (int64_t i = 0; i < x.dim(); i++) {
+        const int64_t a = x.size(i), b = y.size(i);
+        if (a == 1 && b == 1)
+            continue;
+        if (a != 1 && b != 1 && x.stride(i) != y.stride(i))
+            return -1;
+        int at = n++;
+        for (const int64_t step = a != 1 ? x.stride(i) : y.stride(i); at > 0 && d[at - 1].step > step; at--)
+            d[at] = d[at - 1];
+        d[at] = Dim{a != 1 ? x.stride(i) : y.stride(i), a, b};
+    }
+    int64_t extent = 1;
+    for (int i = 0; i < n; i++) {
+        if (d[i].step < extent)
+            return -2;
+        extent = (std::max(d[i].a, d[i].b) - 1) * d[i].step + extent;
+    }
+    return n;
+}
+
+int64_t extent_of(const Tensor &x)
+{
+    int64_t n = 1;
+    for (int64_t i = 0; i < x.dim(); i++)
+        n += (x.size(i) - 1) * x.stride(i);
+    return n;
+}
+
+// Whether x and y, of one type and number of dimensions (at most 4), are known to share memory.
+// `self`: whether that counts where they are the same elements in the same places.
+bool meet(const Tensor &x, const Tensor &y, bool self)
+{
+    if (x.numel() == 0 || y.numel() == 0 || x.device() != y.device())
+        return false;
+    const int64_t size = x.element_size();
+    const char *a = static_cast<const char *>(x.const_data_ptr()), *b = static_cast<const char *>(y.const_data_ptr());
+    if (a + extent_of(x) * size <= b || b + extent_of(y) * size <= a)
+        return false;
+    Dim d[4];
+    const int n = dims_of(x, y, d);
+    if (a == b)
+        return self || n < 0 || x.sizes() != y.sizes();
+    if (n >= 0)
+        return (b - a) % size != 0 || reaches(d, n, (b - a) / size);
+    return x.is_non_overlapping_and_dense() && y.is_non_overlapping_and_dense();
+}
+
+void want_apart(const Tensor &out, const Tensor &in, bool same_input, const char *what)
+{
+    want(!meet(out, in, !same_input), out, what);
+}
+void want_places(const Tensor &out, const char *what)
+{
+    Dim d[4];
+    want(out.numel() == 0 || dims_of(out, out, d) >= 0, out, what);
+}
+
 // The device of the call's tensors and the stream given (a pointer) made current, so that what
 // the call allocates belongs to the stream that uses it: a workspace is free again when the call
 // returns, and only that stream's order keeps the kernel's use before the next one's.
@@ -167,6 +254,10 @@ PyObject *rope(const Args &a)
     Tensor q_out = a.none(7) ? at::empty_like(q) : a.tensor(7, "q_out"), k_out;
     want(q_out.sizes() == q.sizes() && same(q_out, q) && q_out.stride(-1) == 1, q_out,
          "q_out has q's shape, type and device");
+    if (!a.none(7)) {
+        want_places(q_out, "q_out's elements lie apart, the step of each dimension past what lies within it");
+        want_apart(q_out, q, true, "q_out is q itself or lies apart from it");
+    }
     place(0, q);
     place(3, q_out);
     const Tensor *k = nullptr;
@@ -178,6 +269,16 @@ PyObject *rope(const Args &a)
         k_out = a.none(8) ? at::empty_like(*k) : a.tensor(8, "k_out");
         want(k_out.sizes() == k->sizes() && same(k_out, q) && k_out.stride(-1) == 1, k_out,
              "k_out has k's shape, type and device");
+        if (!a.none(8)) {
+            want_places(k_out, "k_out's elements lie apart, the step of each dimension past what lies within it");
+            want_apart(k_out, *k, true, "k_out is k itself or lies apart from it");
+            want_apart(k_out, q, false, "k_out lies apart from q");
+        }
+        if (!a.none(7)) {
+            want_apart(q_out, *k, false, "q_out lies apart from k");
+            if (!a.none(8))
+                want_apart(q_out, k_out, false, "q_out lies apart from k_out");
+        }
         place(6, *k);
         place(9, k_out);
     }
@@ -265,6 +366,12 @@ PyObject *append(const Args &a)
         q_out = a.none(11) ? at::empty_like(*q) : a.tensor(11, "q_out");
         want(q_out.sizes() == q->sizes() && same(q_out, k) && q_out.stride(2) == 1, q_out,
              "q_out has q's shape, type and device");
+        if (!a.none(11)) {
+            want_places(q_out, "q_out's elements lie apart, the step of each dimension past what lies within it");
+            want_apart(q_out, *q, true, "q_out is q itself or lies apart from it");
+            want_apart(q_out, k, false, "q_out lies apart from k");
+            want_apart(q_out, v, false, "q_out lies apart from v");
+        }
         st[4] = q->stride(0);
         st[5] = q->stride(1);
         st[6] = q_out.stride(0);
@@ -313,6 +420,8 @@ PyObject *gather(const Args &a)
         return x;
     };
     Tensor k = out(8, "k_out"), v = out(9, "v_out");
+    if (!a.none(8) && !a.none(9))
+        want_apart(k, v, false, "k_out lies apart from v_out");
     const sage_status_t rc = p_gather(s.cache.const_data_ptr(), s.table_at(), s.lens_at(), s.cu, k.mutable_data_ptr(),
                                       v.mutable_data_ptr(), type == at::kHalf ? SAGE_F16 : SAGE_BF16, s.nseq, total,
                                       s.Hkv, rep, d, s.page_size, s.num_pages, s.max_pages, w.stream());
@@ -335,6 +444,8 @@ PyObject *attn(const Args &a)
     Tensor out = a.none(8) ? at::empty(q.sizes(), q.options()) : a.tensor(8, "out");
     want(out.sizes() == q.sizes() && same(out, q) && out.is_contiguous(), out,
          "out is contiguous and has q's shape, type and device");
+    if (!a.none(8))
+        want_apart(out, q, true, "out is q itself or lies apart from it");
     float *lse = nullptr;
     if (!a.none(9)) {
         const Tensor &x = a.tensor(9, "lse");

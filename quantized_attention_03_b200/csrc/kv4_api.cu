@@ -20,6 +20,16 @@ bool strides_ok(const int64_t *s, int n)
     return true;
 }
 
+// Strides that an output may have over dimensions of n places: none 0, which would put several
+// elements in one place; those of the input where it is the input.
+bool out_strides_ok(const void *in, const int64_t *si, const void *out, const int64_t *so, const int *n, int dims)
+{
+    for (int i = 0; i < dims; i++)
+        if (n[i] > 1 && (so[i] == 0 || (in == out && si[i] != so[i])))
+            return false;
+    return true;
+}
+
 sage_status_t check_rot(int rot_dim, int d, const double *freqs, int flags, int known_flags)
 {
     if (flags & ~known_flags)
@@ -125,6 +135,10 @@ sage_status_t sage_rope(const void *q, void *q_out, const void *k, void *k_out,
     if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) ||
         (strides && !strides_ok(strides, 12)))
         return SAGE_ERR_MISALIGNED;
+    const int nq[3] = {B, Hq, N}, nk[3] = {B, Hk, N};
+    if (strides && ((Hq > 0 && !out_strides_ok(q, strides, q_out, strides + 3, nq, 3)) ||
+                    (Hk > 0 && !out_strides_ok(k, strides + 6, k_out, strides + 9, nk, 3))))
+        return SAGE_ERR_INVALID_ARG;
     auto tensor = [&](const void *in, void *out, int H, const int64_t *s) {
         const int64_t b = (int64_t)H * N * d, h = (int64_t)N * d;
         if (!s)
@@ -171,6 +185,9 @@ sage_status_t sage_kv4_append(void *cache, const int32_t *block_table, const int
     if (!aligned16(cache) || !aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) ||
         !aligned16(k_mean) || (strides && !strides_ok(strides, 8)))
         return SAGE_ERR_MISALIGNED;
+    const int nq[2] = {total, Hq};
+    if (strides && q && !out_strides_ok(q, strides + 4, q_out, strides + 6, nq, 2))
+        return SAGE_ERR_INVALID_ARG;
     int *status = status_ptr(&r);
     if (!status)
         return r;

@@ -224,6 +224,70 @@ def test_wrappers_refuse_wrong_tensors_before_the_library(lib):
             raise AssertionError(i)
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    cache, table, lens, cu = _cpu_sequences()
+    f, _ = sage.rope_freqs(32, device="cpu")
+    buf = torch.zeros(4096, dtype=torch.float16)
+    at = lambda shape, stride, start=0: buf.as_strided(shape, stride, start)  # noqa: E731
+    q, k = at((2, 4, 64), (512, 64, 1)), at((2, 2, 64), (512, 64, 1), 256)     # of one projection
+    other = torch.zeros((2, 4, 64), dtype=torch.float16)
+    wrong = [
+        lambda: sage.rope(q, None, f, q_out=other[:, :1].expand(2, 4, 64)),        # one place for all heads
+        lambda: sage.rope(q, None, f, q_out=at((2, 4, 64), (256, 64, 1), 2048)[:1].expand(2, 4, 64)),
+        lambda: sage.rope(q, None, f, q_out=at((2, 4, 64), (256, 64, 1))),         # q's address, other strides
+        lambda: sage.rope(q, None, f, q_out=at((2, 4, 64), (64, 128, 1))),
+        lambda: sage.rope(q, None, f, q_out=at((2, 4, 64), (512, 64, 1), 64)),     # one head further
+        lambda: sage.rope(q, None, f, q_out=at((2, 4, 64), (512, 64, 1), 512)),    # one token further
+        lambda: sage.rope(q, None, f, q_out=at((2, 4, 64), (512, 64, 1), 8)),      # 8 channels further
+        lambda: sage.rope(other, None, f, q_out=at((2, 4, 64), (32, 64, 1))),      # heads in one another
+        lambda: sage.rope(q[:, :2], k, f, q_out=k),
+        lambda: sage.rope(q[:, :2], k, f, k_out=q[:, :2]),
+        lambda: sage.rope(q, k, f, q_out=other, k_out=other[:, 2:]),
+        lambda: sage.rope(other[None], None, f, q_out=other.as_strided((1, 2, 4, 64), (512, 64, 128, 1))),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q, f, q_out=at((2, 4, 64), (256, 64, 1))),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q, f, q_out=other[:, :1].expand(2, 4, 64)),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, k, q, f, q_out=at((2, 4, 64), (512, 64, 1), 128)),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, other[:, :2], q, f, q_out=other),
+        lambda: sage.kv4_gather(cache, table, lens, cu, 2, 64, k_out=at((2, 2, 64), (128, 64, 1)),
+                                v_out=at((2, 2, 64), (128, 64, 1), 64)),
+        lambda: sage.attn_kv4(q, cache, table, lens, cu, 1, out=at((2, 4, 64), (256, 64, 1))),
+        lambda: sage.attn_kv4(at((2, 4, 64), (256, 64, 1)), cache, table, lens, cu, 1,
+                              out=at((2, 4, 64), (256, 64, 1), 64)),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError, match="apart"):
+            call()
+            raise AssertionError(i)
+    # in place, side by side in one buffer, and places of dimensions of one: past these checks,
+    # to the refusal of CPU tensors
+    fine = [
+        lambda: sage.rope(q, k, f, q_out=q, k_out=k),
+        lambda: sage.rope(q, k, f, q_out=at((2, 4, 64), (512, 64, 1), 2048), k_out=at((2, 2, 64), (512, 64, 1), 2304)),
+        lambda: sage.rope(q[:, :2], k, f, q_out=at((2, 2, 64), (512, 64, 1), 128), k_out=at((2, 2, 64), (512, 64, 1), 384)),
+        lambda: sage.rope(q[:1], None, f, q_out=at((1, 4, 64), (8, 64, 1))),
+        lambda: sage.rope(other[:, :1].expand(2, 4, 64), None, f),
+        lambda: sage.kv4_append(cache, table, lens, cu, k, at((2, 2, 64), (512, 64, 1), 384), q, f, q_out=q),
+        lambda: sage.kv4_gather(cache, table, lens, cu, 2, 64, k_out=at((2, 2, 64), (128, 64, 1)),
+                                v_out=at((2, 2, 64), (128, 64, 1), 256)),
+        lambda: sage.attn_kv4(other, cache, table, lens, cu, 1, out=other),
+    ]
+    for call in fine:
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+
+
+def test_c_calls_refuse_outputs_over_their_input(lib):
+    bad = sage.SAGE_ERR_INVALID_ARG
+    dense = [1024, 512, 128]
+    # q_out = q and k_out = k at 0x10000: other strides, and none for several places
+    assert _rope(lib, strides=dense + [1024, 128, 256] + dense * 2) == bad
+    assert _rope(lib, strides=dense * 3 + [1024, 128, 256]) == bad
+    assert _rope(lib, qo=FAKE + 65536, strides=dense + [1024, 0, 128] + dense * 2) == bad
+    assert _rope(lib, ko=FAKE + 65536, strides=dense * 3 + [1024, 512, 0]) == bad
+    assert _append(lib, strides=[256, 128, 256, 128, 512, 128, 1024, 128]) == bad
+    assert _append(lib, qo=FAKE + 65536, strides=[256, 128, 256, 128, 512, 128, 512, 0]) == bad
+
+
 def test_tensors_of_the_cpu_are_refused(lib):
     cache, table, lens, cu = _cpu_sequences()
     f, _ = sage.rope_freqs(64, device="cpu")
