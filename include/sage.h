@@ -326,7 +326,7 @@ SAGE_API sage_status_t sage_attn_decode_quantized(const int8_t *q_i8, const floa
  * attention: sage_rope rotates queries and keys; sage_kv4_append rotates new queries and
  * keys and writes keys and values into a paged cache in 4 bits; sage_attn_kv4 is the
  * attention of a few new queries per sequence over that cache; sage_kv4_gather reads the
- * cache back as 16-bit tensors, e.g. for sage_attn_varlen_fwd_kv of a prefill chunk.
+ * cache back as 16-bit tensors, in fp16 e.g. for sage_attn_varlen_fwd_kv of a prefill chunk.
  * Tensors are fp16 (dtype SAGE_F16) or bf16 (SAGE_BF16), head dim 64 or 128. Nothing here
  * allocates; make the first call on each device before any stream capture. Kernels may start
  * while the one before them in the stream runs down (programmatic stream serialization) and
@@ -428,8 +428,8 @@ SAGE_API sage_status_t sage_kv4_append(void *cache, const int32_t *block_table,
 
 /*
  * Gather: the last tokens of every sequence as k_out and v_out [total, Hkv*rep, d], each head
- * written rep times side by side, Hkv*rep at most 65535 (for attention entry points that take as many key heads as
- * query heads). With cu_seqlens the running sum of kv_lens: all of them. Allocates nothing.
+ * written rep times side by side, Hkv*rep at most 65535 (for attention entry points that take
+ * as many key heads as query heads; those of this header read fp16). With cu_seqlens the running sum of kv_lens: all of them. Allocates nothing.
  */
 SAGE_API sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_table,
                                        const int32_t *kv_lens, const int32_t *cu_seqlens,

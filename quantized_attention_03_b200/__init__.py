@@ -406,6 +406,26 @@ def _smooth_flags(smooth_k: bool, smooth_v: bool, fine: bool = False,
             | (SAGE_QK_FINE if fine else 0) | (SAGE_SMOOTH_Q if smooth_q else 0))
 
 
+def _want_fp16(q, k=None, v=None, out=None):
+    """What goes to the attention and quantization kernels by address alone is contiguous
+    float16, and k and v have q's heads and channels (and a dense q's batch), and one length."""
+    import torch
+    for x in (q, k, v, out):
+        if x is not None and (x.dtype is not torch.float16 or not x.is_contiguous()):
+            raise ValueError(f"contiguous float16 tensors are wanted, got {x.dtype} {tuple(x.shape)} with "
+                             f"strides {x.stride()}")
+
+    def heads(x):
+        return x.shape[1:] if x.dim() == 3 else x.shape[:2] + x.shape[3:]
+
+    if k is not None and (k.dim() != q.dim() or heads(k) != heads(q)):
+        raise ValueError(f"k has q's heads and channels, got {tuple(k.shape)} and {tuple(q.shape)}")
+    if v is not None and k is not None and v.shape != k.shape:
+        raise ValueError(f"v has k's shape, got {tuple(v.shape)} and {tuple(k.shape)}")
+    if out is not None and out.shape != q.shape:
+        raise ValueError(f"out has q's shape, got {tuple(out.shape)} and {tuple(q.shape)}")
+
+
 def sageattn(q, k, v, causal: bool = False, smooth_k: bool = True, pv_mode: int = SAGE_PV_FP16,
              sm_scale: float = 0.0, out=None, stream=None, smooth_v: bool = False,
              fine: bool = False, smooth_q: bool = False):
@@ -414,6 +434,7 @@ def sageattn(q, k, v, causal: bool = False, smooth_k: bool = True, pv_mode: int 
     import torch
     B, H, Nq, d = q.shape
     Nk = k.shape[2]
+    _want_fp16(q, k, v, out)
     if out is None:
         out = torch.empty_like(q)
     flags = _smooth_flags(smooth_k, smooth_v, fine, smooth_q)
@@ -436,6 +457,7 @@ def sageattn_varlen_kv(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, m
     import torch
     Tq, H, d = q.shape
     Tk = k.shape[0]
+    _want_fp16(q, k, v, out)
     if out is None:
         out = torch.empty_like(q)
     sage_attn_varlen_fwd_kv(q, k, v, out, cu_seqlens_q, cu_seqlens_k, cu_seqlens_q.numel() - 1,
@@ -453,6 +475,9 @@ def sageattn_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False,
     The options are sageattn's."""
     import torch
     T, H, d = q.shape
+    _want_fp16(q, k, v, out)
+    if k.shape != q.shape:
+        raise ValueError(f"k has q's shape, got {tuple(k.shape)} and {tuple(q.shape)}")
     if out is None:
         out = torch.empty_like(q)
     sage_attn_varlen_fwd(q, k, v, out, cu_seqlens, cu_seqlens.numel() - 1, T, max_seqlen, H, d,
@@ -469,6 +494,7 @@ def quant_qk(q, k, smooth_k: bool = True, stream=None, fine: bool = False,
     import torch
     B, H, N, d = q.shape
     Nk = k.shape[2]
+    _want_fp16(q, k)
     dev = q.device
     qg, kg = (1, 32) if fine else (Q_BLOCK, K_BLOCK)
     z = dict(q_i8=torch.empty(q.shape, dtype=torch.int8, device=dev),
@@ -496,6 +522,7 @@ def quant_qk_varlen(q, k, cu_seqlens, max_seqlen: int, smooth_k: bool = True, st
     import torch
     T, H, d = q.shape
     nseq = cu_seqlens.numel() - 1
+    _want_fp16(q, k)
     dev = q.device
     qg, kg = (1, 32) if fine else (Q_BLOCK, K_BLOCK)
     z = dict(q_i8=torch.empty(q.shape, dtype=torch.int8, device=dev),
@@ -516,6 +543,7 @@ def quant_v_fp8(v, stream=None, smooth_v: bool = False):
     smooth_v, a third result: the channel mean of V [B,H,d] the codes are taken from."""
     import torch
     B, H, N, d = v.shape
+    _want_fp16(v)
     codes = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
     scales = torch.empty((B, H, d), dtype=torch.float32, device=v.device)
     if not smooth_v:
@@ -530,6 +558,7 @@ def quant_v_fp8_varlen(v, cu_seqlens, max_seqlen: int, stream=None, smooth_v: bo
     import torch
     T, H, d = v.shape
     nseq = cu_seqlens.numel() - 1
+    _want_fp16(v)
     codes = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
     scales = torch.empty((nseq, H, d), dtype=torch.float32, device=v.device)
     if not smooth_v:
@@ -549,6 +578,8 @@ def attn_quantized(q_i8, q_scale, k_i8, k_scale, v, v_scale, causal: bool = Fals
     import torch
     B, H, N, d = q_i8.shape
     Nk = k_i8.shape[2]
+    if pv_mode == SAGE_PV_FP16:
+        _want_fp16(v)
     if out is None:
         out = torch.empty(q_i8.shape, dtype=torch.float16, device=q_i8.device)
     if Nk != N or fine or q_comp is not None:
@@ -575,6 +606,7 @@ def attn_decode(q_i8, q_scale, k_i8, k_scale, v, causal: bool = False, sm_scale:
     import torch
     B, H, Nq, d = q_i8.shape
     Nk = k_i8.shape[2]
+    _want_fp16(v)
     if out is None:
         out = torch.empty(q_i8.shape, dtype=torch.float16, device=q_i8.device)
     need = sage_attn_decode_workspace_size(B, H, Nq, Nk, d)
@@ -673,8 +705,9 @@ def kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q=None, freqs=None
 def kv4_gather(cache, block_table, kv_lens, cu_seqlens, total: int, d: int, dtype=None,
                rep: int = 1, k_out=None, v_out=None, stream=None):
     """The last cu_seqlens[s+1] - cu_seqlens[s] tokens of every sequence as 16-bit k and v
-    [total, Hkv * rep, d], each head rep times (dtype float16 by default): what
-    sageattn_varlen_kv takes for a prefill chunk over cached keys."""
+    [total, Hkv * rep, d], each head rep times, d that of kv4_cache. In float16 (the default)
+    they are what sageattn_varlen_kv takes, with float16 queries, for a prefill chunk over
+    cached keys; this package's prefill attention takes no bfloat16."""
     import torch
     if dtype not in (None, torch.float16, torch.bfloat16):
         raise ValueError(f"dtype is float16 or bfloat16, got {dtype}")

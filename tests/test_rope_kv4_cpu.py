@@ -307,3 +307,40 @@ def test_missing_binding_fails_loudly(lib, monkeypatch):
     monkeypatch.setitem(sys.modules, "quantized_attention_03_b200._binding", None)
     with pytest.raises(RuntimeError, match="_binding.so"):
         sage.rope(torch.zeros((1, 1, 64), dtype=torch.float16), None, torch.zeros(32, dtype=torch.float64))
+
+
+def test_fp16_calls_refuse_what_the_cache_calls_give_in_bf16(lib):
+    # the attention and quantization calls pass addresses on: bf16, or a strided view (a
+    # projection rotated in place), would be read as contiguous fp16
+    half = lambda *shape: torch.zeros(shape, dtype=torch.float16)  # noqa: E731
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    q, k = half(4, 4, 64), half(4, 4, 64)
+    dq, dk = half(1, 4, 4, 64), half(1, 4, 8, 64)
+    codes, scales = torch.zeros((1, 4, 4, 64), dtype=torch.int8), torch.zeros((1, 4, 1))
+    b, view = torch.bfloat16, half(4, 8, 64)[:, :4]
+    wrong = [
+        lambda: sage.sageattn_varlen_kv(q.to(b), k, k, cu, cu, 4, 4),
+        lambda: sage.sageattn_varlen_kv(q, k.to(b), k.to(b), cu, cu, 4, 4),
+        lambda: sage.sageattn_varlen_kv(q, k, k.to(b), cu, cu, 4, 4),
+        lambda: sage.sageattn_varlen_kv(view, k, k, cu, cu, 4, 4),
+        lambda: sage.sageattn_varlen_kv(q, k, k, cu, cu, 4, 4, out=q.to(b)),
+        lambda: sage.sageattn_varlen_kv(q, half(4, 2, 64), half(4, 2, 64), cu, cu, 4, 4),      # heads not repeated
+        lambda: sage.sageattn_varlen_kv(q, k, k[:3], cu, cu, 4, 4),
+        lambda: sage.sageattn_varlen(q.to(b), k.to(b), k.to(b), cu, 4),
+        lambda: sage.sageattn_varlen(q, half(3, 4, 64), half(3, 4, 64), cu, 4),
+        lambda: sage.sageattn_varlen(q, k, k, cu, 4, out=q[:3]),
+        lambda: sage.sageattn(dq.to(b), dk, dk),
+        lambda: sage.sageattn(dq, dk, dk.to(b)),
+        lambda: sage.sageattn(dq.transpose(1, 2), dk, dk),
+        lambda: sage.sageattn(dq, dk[:, :2].contiguous(), dk[:, :2].contiguous()),
+        lambda: sage.quant_qk(dq.to(b), dk.to(b)),
+        lambda: sage.quant_qk_varlen(q, k.to(b), cu, 4),
+        lambda: sage.quant_v_fp8(dk.to(b)),
+        lambda: sage.quant_v_fp8_varlen(k.to(b), cu, 4),
+        lambda: sage.attn_quantized(codes, scales, codes, scales, dq.to(b), None),
+        lambda: sage.attn_decode(codes, scales, codes, scales, dq.to(b)),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(i)

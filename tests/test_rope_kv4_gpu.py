@@ -719,3 +719,30 @@ def test_the_longest_sequence():
     assert (last == 1).all()
     want = torch.full((1, 1, 64), 1 - 64 * 2 ** 23 / n, dtype=torch.float64)
     near(out, want, 2 * 151_000 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("d,page,Hkv,rep", [(128, 64, 2, 4), (64, 16, 3, 1)])
+def test_prefill_over_the_cache_is_attention_over_what_it_stands_for(d, page, Hkv, rep):
+    # a chunk of new tokens over cached ones: the package's attention has the same bits over
+    # gathered keys and values as over the cache's values worked out on the CPU (code times step
+    # is exact in 32 bits, the sum with low and the fp16 result are each rounded once)
+    lens, news = [300, 45, 129], [200, 45, 1]
+    w = World(lens, news, Hkv, d, page, seed=21)
+    w.fill(offset=0.5)
+    table, kv_lens, cu = w.where()
+    cu_all = torch.cumsum(torch.tensor([0] + lens), 0).to(torch.int32).cuda()
+    total = sum(lens)
+    kg, vg = sage.kv4_gather(w.cache.cuda(), table, kv_lens, cu_all, total, d, rep=rep)
+    parts = [w.tokens(s, dtype=torch.float32) for s in range(len(lens))]
+    want = [torch.cat([p[x] for p in parts]).to(F16).repeat_interleave(rep, 1) for x in (0, 1)]
+    assert torch.equal(kg.cpu(), want[0]) and torch.equal(vg.cpu(), want[1])
+    q = torch.randn((w.total, Hkv * rep, d), generator=w.g).to(F16).cuda()
+    got = sage.sageattn_varlen_kv(q, kg, vg, cu, cu_all, max(news), max(lens), causal=True)
+    same = sage.sageattn_varlen_kv(q, want[0].cuda(), want[1].cuda(), cu, cu_all, max(news), max(lens), causal=True)
+    ok()
+    assert torch.equal(got, same)
+    for s, n in enumerate(news):                        # and near the 64-bit attention over it
+        a = int(w.cu[s])
+        exact, _, _, _ = ref.attend(q[a:a + n].cpu().double(), *(x.double().repeat_interleave(rep, 1) for x in parts[s]))
+        off = got[a:a + n].cpu().double() - exact
+        assert float(off.norm() / exact.norm()) < 0.02
