@@ -672,11 +672,62 @@ def rope(q, k, freqs, positions=None, mscale: float = 1.0, interleaved: bool = F
     """Rotary positions of q [B, Hq, N, d] and k [B, Hk, N, d], or packed [T, H, d] (any
     strides; k may be None): (q_out, k_out). freqs and mscale: rope_freqs. positions int32 [N],
     [B, N] or [T]; None: 0 .. N-1. interleaved: pairs (2i, 2i+1), else (i, i + rot/2). inverse:
-    the rotation back, which is also its gradient. q_out=q, k_out=k rotates in place; outputs
-    that overlap inputs or each other otherwise raise ValueError where that can be seen."""
-    return _done("sage_rope", (_calls or _bound()).rope(
-        q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out,
-        None if stream is None else _stream(stream)))
+    by the negative angles, with the same mscale: the transpose of the rotation, which is its
+    gradient (and at mscale 1 the way back). Autograd goes through the call: where q or k
+    requires a gradient, so do the results, and q_out and k_out cannot be given. q_out=q,
+    k_out=k rotates in place; outputs that overlap inputs or each other otherwise raise
+    ValueError where that can be seen."""
+    r = (_calls or _bound()).rope(q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out,
+                                  None if stream is None else _stream(stream))
+    if r == -1:
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out take no gradient")
+        return _rope_autograd(q, k, freqs, positions, mscale, interleaved, inverse, stream)
+    return _done("sage_rope", r)
+
+
+_rope_function = None
+
+
+def _rope_autograd(q, k, freqs, positions, mscale, interleaved, inverse, stream):
+    """rope as a node of autograd's graph; its backward is rope again, with the other angles."""
+    global _rope_function
+    import torch
+    if _rope_function is None:
+        class Rope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, freqs, positions, mscale, interleaved, inverse):
+                ctx.set_materialize_grads(False)
+                ctx.save_for_backward(freqs, positions)
+                ctx.how = mscale, interleaved, inverse
+                out = rope(q, k, freqs, positions, mscale, interleaved, inverse)
+                ctx.mark_non_differentiable(*(x for x, need in zip(out, ctx.needs_input_grad)
+                                              if x is not None and not need))
+                return out
+
+            @staticmethod
+            def backward(ctx, q, k):
+                mscale, interleaved, inverse = ctx.how
+                freqs, positions = ctx.saved_tensors
+                # a gradient comes in whatever layout the graph gave it
+                x = [g if g is None or (g.stride(-1) == 1 and all(s % 8 == 0 for s in g.stride()[:-1])
+                                        and g.data_ptr() % 16 == 0)
+                     else g.clone(memory_format=torch.contiguous_format)
+                     for g in (g if need else None for g, need in zip((q, k), ctx.needs_input_grad))]
+                if x[0] is not None:
+                    x = rope(x[0], x[1], freqs, positions, mscale, interleaved, not inverse)
+                elif x[1] is not None:
+                    x = None, rope(x[1], None, freqs, positions, mscale, interleaved, not inverse)[0]
+                return *x, None, None, None, None, None
+
+        _rope_function = Rope
+    args = q, k, freqs, positions, mscale, interleaved, inverse
+    if stream is None:
+        return _rope_function.apply(*args)
+    raw = _stream(stream)                               # the backward pass runs on it too
+    with torch.cuda.stream(torch.cuda.default_stream(q.device) if raw == 0
+                           else torch.cuda.ExternalStream(raw, q.device)):
+        return _rope_function.apply(*args)
 
 
 def kv4_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):

@@ -4,6 +4,7 @@
 // returns its outputs, or the library's status code as an int when the call was refused.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -234,10 +235,20 @@ const double *freqs_of(const Args &a, int i, const Tensor &x, int &rot)
     return static_cast<const double *>(f.const_data_ptr());
 }
 
-// (q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out, stream)
+// (q, k, freqs, positions, mscale, interleaved, inverse, q_out, k_out, stream); -1 instead of a
+// status where a gradient of q or k is wanted: the caller goes through autograd then
 PyObject *rope(const Args &a)
 {
     const Tensor &q = a.tensor(0, "q");
+    if (at::GradMode::is_enabled()) {
+        if (!a.none(2) && a.tensor(2, "freqs").requires_grad())
+            throw Refused("freqs takes no gradient");
+        if (q.requires_grad() || (!a.none(1) && a.tensor(1, "k").requires_grad()))
+            return PyLong_FromLong(-1);
+        for (int i : {7, 8})
+            if (!a.none(i) && a.tensor(i, "q_out and k_out").requires_grad())
+                throw Refused("q_out and k_out take no gradient");
+    }
     const int type = half_type(q, "q is float16 or bfloat16");
     const bool packed = q.dim() == 3;
     want((packed || q.dim() == 4) && q.stride(-1) == 1, q,

@@ -344,3 +344,17 @@ def test_fp16_calls_refuse_what_the_cache_calls_give_in_bf16(lib):
         with pytest.raises(ValueError):
             call()
             raise AssertionError(i)
+
+
+def test_rope_takes_no_gradient_for_what_has_none(lib):
+    f, _ = sage.rope_freqs(64, device="cpu")
+    x = torch.zeros((2, 2, 64), dtype=torch.float16)
+    leaf = x.clone().requires_grad_()
+    for call in (lambda: sage.rope(leaf, None, f, q_out=x), lambda: sage.rope(x, leaf, f, k_out=x.clone()),
+                 lambda: sage.rope(x, None, f, q_out=leaf), lambda: sage.rope(x, None, f.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
+        sage.rope(leaf, None, f, q_out=x)
+    with pytest.raises(ValueError, match="CUDA device"):
+        sage.rope(leaf, leaf, f)

@@ -131,6 +131,116 @@ def test_rope_inverse_is_the_gradient(inter):
     ok()
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("inter,inv,rot", [(False, False, 128), (True, True, 64)])
+def test_rope_in_autograd(packed, inter, inv, rot):
+    g = torch.Generator().manual_seed(rot + packed)
+    rnd = lambda *shape: torch.randn(shape, generator=g).to(F16).cuda()  # noqa: E731
+    shape = (lambda h: (40, h, 128)) if packed else (lambda h: (2, h, 20, 128))
+    q, k = rnd(*shape(6)).requires_grad_(), rnd(*shape(2)).requires_grad_()
+    gq, gk = rnd(*shape(6)), rnd(*shape(2))
+    pos = torch.randint(0, 9000, (40,) if packed else (2, 20), generator=g, dtype=torch.int32).cuda()
+    freqs, m = sage.rope_freqs(rot, scaling="parts", factor=8.0, original_len=512)
+    how = (freqs, pos, m, inter)
+    plain = sage.rope(q.detach(), k.detach(), *how, inv)
+    back = sage.rope(gq, gk, *how, not inv)
+    assert not plain[0].requires_grad and not plain[1].requires_grad
+    out = sage.rope(q, k, *how, inv)
+    assert out[0].requires_grad and out[1].requires_grad
+    assert torch.equal(out[0], plain[0]) and torch.equal(out[1], plain[1])
+    got = torch.autograd.grad(out, (q, k), (gq, gk), retain_graph=True)
+    assert torch.equal(got[0], back[0]) and torch.equal(got[1], back[1])
+    # one of the two results used, and one of the two inputs differentiated
+    assert torch.equal(torch.autograd.grad(out[0], q, gq, retain_graph=True)[0], back[0])
+    assert torch.equal(torch.autograd.grad(out[1], k, gk, retain_graph=True)[0], back[1])
+    assert torch.autograd.grad(out[1], q, gk, allow_unused=True)[0] is None
+    qo, ko = sage.rope(q.detach(), k, *how, inv)
+    assert not qo.requires_grad and torch.equal(qo, plain[0])
+    assert torch.equal(torch.autograd.grad(ko, k, gk)[0], back[1])
+    qo, ko = sage.rope(q, None, *how, inv)
+    assert ko is None and torch.equal(torch.autograd.grad(qo, q, gq)[0], back[0])
+    with torch.no_grad():
+        assert not sage.rope(q, k, *how, inv)[0].requires_grad
+    ok()
+
+
+def test_rope_gradients_in_any_layout_and_of_views():
+    # an expanded gradient (of a sum), a transposed one, one off its alignment; a key head that
+    # all query heads share, and projections of one buffer
+    g = torch.Generator().manual_seed(5)
+    fused = torch.randn((24, 8, 64), generator=g).to(F16).cuda().requires_grad_()
+    pos = torch.arange(24, dtype=torch.int32).cuda()
+    freqs, _ = sage.rope_freqs(64)
+    one = fused[:, 6:7]
+    q, k = sage.rope(fused[:, :6], one.expand(24, 6, 64), freqs, pos)
+    want = lambda y: sage.rope(y.clone(memory_format=torch.contiguous_format), None, freqs, pos, inverse=True)[0]  # noqa: E731
+    ones = torch.ones((24, 6, 64), dtype=F16, device="cuda")
+    grad, = torch.autograd.grad(q.sum() + k.sum(), fused, retain_graph=True)
+    assert torch.equal(grad[:, :6], want(ones)) and (grad[:, 7] == 0).all()
+    near(grad[:, 6], want(ones).double().sum(1).cpu(), 6 * 2.0 ** -10 * 6)
+    odd = torch.randn(24 * 6 * 64 + 1, generator=g).to(F16).cuda()[1:].view(24, 6, 64)
+    turned = torch.randn((64, 6, 24), generator=g).to(F16).cuda().permute(2, 1, 0)
+    for y in (odd, turned):
+        grad, = torch.autograd.grad(q, fused, y, retain_graph=True)
+        assert torch.equal(grad[:, :6], want(y))
+    ok()
+
+
+def test_rope_gradient_twice_on_a_stream_and_after_its_inputs_changed():
+    g = torch.Generator().manual_seed(6)
+    x, y = (torch.randn((12, 2, 64), generator=g).to(F16).cuda() for _ in range(2))
+    freqs, m = sage.rope_freqs(64, scaling="parts", factor=4.0, original_len=2048)
+    pos = torch.arange(12, dtype=torch.int32).cuda()
+    x.requires_grad_()
+    # the gradient is linear in y: its gradient towards y is the rotation itself
+    y.requires_grad_()
+    out, _ = sage.rope(x, None, freqs, pos, m)
+    grad, = torch.autograd.grad(out, x, y, create_graph=True)
+    again, = torch.autograd.grad(grad, y, x.detach())
+    assert torch.equal(again, out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        leaf = x.detach().requires_grad_()
+        there, _ = sage.rope(leaf, None, freqs, pos, m, stream=stream)
+        got, = torch.autograd.grad(there, leaf, y.detach())
+        torch.cuda.synchronize()
+        assert torch.equal(there, out) and torch.equal(got, grad)
+    # positions that were moved on since are noticed, as autograd does
+    pos.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(out, x, y)
+    ok()
+
+
+def test_rope_gradient_in_a_captured_graph():
+    g = torch.Generator().manual_seed(7)
+    x, y = (torch.randn((33, 4, 128), generator=g).to(BF16).cuda() for _ in range(2))
+    freqs, _ = sage.rope_freqs(128)
+    pos = torch.arange(33, dtype=torch.int32).cuda()
+
+    def step():
+        leaf = x.detach().requires_grad_()
+        out, _ = sage.rope(leaf, None, freqs, pos)
+        return out, torch.autograd.grad(out, leaf, y)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, grad = step()
+    for _ in range(2):
+        x.copy_(torch.randn(x.shape, generator=g))
+        y.copy_(torch.randn(y.shape, generator=g))
+        graph.replay()
+        assert torch.equal(out, sage.rope(x, None, freqs, pos)[0])
+        assert torch.equal(grad, sage.rope(y, None, freqs, pos, inverse=True)[0])
+    ok()
+
+
 def test_rope_far_positions():
     # 2^30 turns the fastest pair 1.7e8 times; a 32-bit angle would be off by 64
     d = 64
