@@ -21,7 +21,11 @@
 //     an addition for every two, took 260 us).
 //   - Probabilities times step are split into two fp16 terms, high and low, each with its own
 //     product: one term alone would round every p to 11 bits, as much error again as the
-//     rounding of the 16-bit output.
+//     rounding of the 16-bit output. They are scaled by a power of two of their group's largest
+//     step so far, whose product with p = 1 then is 8 or more: two terms are good to 2^-21 of the
+//     product or to 2^-25, which is 2^-28 of the largest step, whichever is more. (One scale for both groups of d = 128
+//     took a group whose values were 10^6 times smaller to 7 bits; two cost the longest cache
+//     2.4 us of 245 and saved the ragged sequences below 0.7 of 81.4.)
 // Queries are the 8-wide side of mma.m16n8k16 and keys (or channels) the 16-wide one, so a
 // group of up to 8 query rows that share a key head costs one pass; the 64-row or 128-row
 // tiles of tcgen05 would be almost empty here and could take the codes only from shared
@@ -575,11 +579,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             }
         }
         const float2 low_sel = t4 < 2 ? make_float2(0.0f, 0.0f) : make_float2(-1.0f, -1.0f);
-        // exponent the value products are scaled for; steps from vlimit on (as fp16 bits) are too
-        // large for it
-        int vexp = -64;
-        uint32_t vlimit = 0;
-        float vscale = 1.0f;
+        // exponents the value products are scaled for, one for each group of channels, so that a
+        // group of small values keeps its bits beside one of large ones; steps from vlimit on (as
+        // fp16 bits) are too large for it
+        int vexp[kG];
+        uint32_t vlimit[kG];
+        float vscale[kG];
+#pragma unroll
+        for (int gr = 0; gr < kG; gr++) {
+            vexp[gr] = -64;
+            vlimit[gr] = 0;
+            vscale[gr] = 1.0f;
+        }
 
         for (int t = seg.t0 + place; t < end; t += step) {
             const int k0 = t * C::kTile;
@@ -667,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                             x[i][c] = fmaxf(x[i][c], fmaxf(s[kb][i][c], s[kb][i][c + 2]));
                         move |= fmaf(x[i][c], f[i][c], nm[i][c]) > 8.0f;
                     }
-                // ---- the tile's largest value step: products p * step are scaled by a power of two
+                // ---- the tile's largest value steps: products p * step are scaled by a power of two
                 // that keeps them below 2^15, whatever V's size. In a masked tile, rows behind the last
                 // token and non-finite steps do not count (elsewhere every row sees every step)
                 const uint2 vraw = reinterpret_cast<const uint2 *>(st + C::kTile * D + C::kParBytes)[lane];
@@ -678,15 +689,20 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                     if (vs.y >= 0x7C00u || k0 + (2 * lane + 1) / kG >= len)
                         vs.y = 0;
                 }
-                const uint32_t vtop = max(vs.x, vs.y);
-                if (__any_sync(0xffffffffu, move || vtop >= vlimit)) {
-                    const int texp = (int)(__reduce_max_sync(0xffffffffu, vtop) >> 10);
-                    float shift = 1.0f;
-                    if (texp > vexp + 3) {
-                        shift = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
-                        vexp = texp;
-                        vlimit = (uint32_t)(vexp + 4) << 10;
-                        vscale = __uint_as_float((uint32_t)(127 + 18 - vexp) << 23);
+                // this lane's two steps: the groups of one key, or two keys' (D = 64)
+                const uint32_t vtop[2] = {kG == 2 ? vs.x : max(vs.x, vs.y), kG == 2 ? vs.y : 0u};
+                if (__any_sync(0xffffffffu, move || vtop[0] >= vlimit[0] || (kG == 2 && vtop[1] >= vlimit[kG - 1]))) {
+                    float shift[kG];
+#pragma unroll
+                    for (int gr = 0; gr < kG; gr++) {
+                        const int texp = (int)(__reduce_max_sync(0xffffffffu, vtop[gr]) >> 10);
+                        shift[gr] = 1.0f;
+                        if (texp > vexp[gr] + 3) {
+                            shift[gr] = vexp[gr] < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp[gr] - texp) << 23);
+                            vexp[gr] = texp;
+                            vlimit[gr] = (uint32_t)(texp + 4) << 10;
+                            vscale[gr] = __uint_as_float((uint32_t)(127 + 18 - texp) << 23);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < NT; i++)
@@ -706,8 +722,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                                 o2[i][gr][c] *= alpha;
 #pragma unroll
                                 for (int j = 0; j < 4; j++) {
-                                    o[i][gr][j][c] *= alpha * shift;
-                                    o[i][gr][j][c + 2] *= alpha * shift;
+                                    o[i][gr][j][c] *= alpha * shift[gr];
+                                    o[i][gr][j][c + 2] *= alpha * shift[gr];
                                 }
                             }
                         }
@@ -717,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                 {
                     const float2 x = __half22float2(bits_h2(vraw.x)), y = __half22float2(bits_h2(vraw.y));
                     reinterpret_cast<float4 *>(vpar)[lane] =
-                        make_float4(x.x * vscale, fmaf(8.0f, x.x, x.y), y.x * vscale, fmaf(8.0f, y.x, y.y));
+                        make_float4(x.x * vscale[0], fmaf(8.0f, x.x, x.y), y.x * vscale[kG - 1], fmaf(8.0f, y.x, y.y));
                     __syncwarp();
                 }
 
@@ -847,7 +863,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             const int64_t last = seg.x + cost + seg.nt;
             tail = Tail{(int)((last * teams + total - 1) / total) - 1, seg.row0, seg.n, seg.kvh, seg.rb};
         }
-        const float unscale = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + 6 + vexp) << 23);
+        float unscale[kG];
+#pragma unroll
+        for (int gr = 0; gr < kG; gr++)
+            unscale[gr] = vexp[gr] < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + 6 + vexp[gr]) << 23);
         float *const part = p.part + (int64_t)(team * 2 + (seg.t0 == 0)) * (C::kRows * C::kPitch);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
@@ -876,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                             float y = o[i][gr][j][c + 2 * e];
                             if (FOLD)
                                 y += __shfl_xor_sync(0xffffffffu, y, 2);
-                            v[gr][2 * j + e] = fmaf(y, e ? unscale * 0.0625f : unscale, ow[gr]);
+                            v[gr][2 * j + e] = fmaf(y, e ? unscale[gr] * 0.0625f : unscale[gr], ow[gr]);
                         }
                 if (r >= nrows || (FOLD && t4 >= 2))
                     continue;

@@ -60,3 +60,24 @@ def test_the_limits_show_planted_mistakes(n, H, d, sharp):
     half = torch.where(torch.arange(n) < n // 2, 1.01, 1.0).double()
     assert ref.misses(result(w * half), out, limit)[0] > 0
     assert ref.misses(torch.zeros_like(out), out, limit)[0] == limit.numel()
+
+
+def test_the_limits_show_a_group_that_lost_its_bits_to_another():
+    # the second group's values a millionth of the first's; one scale for both ends the weights'
+    # products at 2^-28 of the first's step
+    g = torch.Generator().manual_seed(3)
+    scale = torch.cat((torch.full((64,), 100.0), torch.full((64,), 1e-4)))
+    k, v, key_span, value_span, p = cached(700, 1, 128, g, scale)
+    q = torch.randn((2, 4, 128), generator=g).to(BF16)
+    args = (q, k, v, key_span, value_span, p[..., 0], BF16)
+    out, limit, _, _ = ref.room(*args, causal=False)
+    w = weights(q, k, 1 / math.sqrt(128))
+    step, mid = p[:, 0, 1, 0], p[:, 0, 1, 1] + 8 * p[:, 0, 1, 0]
+    code = ((v[:, 0, 64:] - mid[:, None]) / step[:, None]).round()
+    quantum = 2.0 ** -27 * p[:, 0, 0, 0].max()
+    t = torch.round(w * step / quantum) * quantum
+    got = out.clone()
+    got[..., 64:] = (torch.einsum("ihj,jc->ihc", t, code) + torch.einsum("ihj,j->ih", w, mid)[..., None]) / w.sum(-1, keepdim=True)
+    assert ref.misses(out.to(BF16), out, limit)[0] == 0
+    far = (got.to(BF16).double() - out).unflatten(-1, (-1, 64)).norm(dim=-1) / limit
+    assert (far[..., 0] <= 1).all() and (far[..., 1] > 1).all()

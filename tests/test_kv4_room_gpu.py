@@ -96,6 +96,22 @@ def test_most_queries_left_to_the_call(Hq, Hkv, news):
     check(w, q, *attend(w, q, None))
 
 
+@pytest.mark.parametrize("ratio", [1e3, 1e6, 1e8])
+@pytest.mark.parametrize("Hq", [2, 8, 16])
+def test_groups_of_channels_of_very_different_size(Hq, ratio):
+    # values of one half of the channels `ratio` times smaller than those of the other
+    w = World([700, 90, 2100], [1, 1, 1], 2, 128, 32, seed=36)
+    for s, n in enumerate(w.lens):
+        k, v = (torch.randn((n, 2, 128), generator=w.g) for _ in range(2))
+        v[:, 0, :64] *= 1e3 / ratio
+        v[:, 0, 64:] *= 1e3
+        v[:, 1, :64] *= 1e3
+        v[:, 1, 64:] *= 1e3 / ratio
+        w.put(s, torch.arange(n), k, v)
+    q = torch.randn((3, Hq, 128), generator=w.g).to(BF16)
+    check(w, q, *attend(w, q, 1))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_tokens_of_very_different_size(d):
     w = World([1100, 333], [2, 2], 2, d, 64, seed=37)
