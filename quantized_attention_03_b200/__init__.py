@@ -637,6 +637,10 @@ def _bound():
     except ImportError as e:
         raise RuntimeError("quantized_attention_03_b200/_binding.so is missing or does not fit this torch: "
                            "build it with `python -m quantized_attention_03_b200.build`") from e
+    from .build import binding_for
+    if b.built_for != binding_for():
+        raise RuntimeError(f"quantized_attention_03_b200/_binding.so is built for {b.built_for}, this is "
+                           f"{binding_for()}: build it with `python -m quantized_attention_03_b200.build`")
     L = lib()
     b.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
         "sage_rope", "sage_kv4_append", "sage_kv4_gather", "sage_attn_kv4", "sage_attn_kv4_workspace_size")))

@@ -28,10 +28,24 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def binding_for() -> str:
+    """What a binding fits: the Python and the torch that it is compiled against."""
+    import sysconfig
+
+    import torch
+    return (f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__} "
+            f"cxx11abi {int(torch.compiled_with_cxx11_abi())}")
+
+
 def _binding_stale() -> bool:
     deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "sage.h")]
-    return not os.path.exists(BINDING) or any(
-        os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps)
+    if not os.path.exists(BINDING) or any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps):
+        return True
+    try:
+        with open(BINDING + ".for") as f:
+            return f.read() != binding_for()
+    except OSError:
+        return True
 
 
 def build_binding(force: bool = False) -> str:
@@ -49,13 +63,15 @@ def build_binding(force: bool = False) -> str:
     lib = os.path.join(base, "lib")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DBUILT_FOR="{binding_for()}"',
            *(x for p in include for x in ("-isystem", p)), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
            "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError("g++ failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(binding_for())
     return BINDING
 
 

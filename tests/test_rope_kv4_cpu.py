@@ -358,3 +358,14 @@ def test_rope_takes_no_gradient_for_what_has_none(lib):
         sage.rope(leaf, None, f, q_out=x)
     with pytest.raises(ValueError, match="CUDA device"):
         sage.rope(leaf, leaf, f)
+
+
+def test_a_binding_for_another_torch_is_built_again_and_not_used(lib, monkeypatch):
+    from quantized_attention_03_b200 import build
+    assert not build._binding_stale()
+    sage._bound()
+    monkeypatch.setattr(build, "binding_for", lambda: "another python and torch")
+    assert build._binding_stale()
+    monkeypatch.setattr(sage, "_calls", None)
+    with pytest.raises(RuntimeError, match="is built for"):
+        sage.rope(torch.zeros((1, 1, 64), dtype=torch.float16), None, torch.zeros(32, dtype=torch.float64))
