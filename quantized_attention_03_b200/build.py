@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -85,9 +86,21 @@ def _stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source into one shared library (objects built in parallel), and the
-    Python extension beside it."""
-    build_binding(force)
+    """Compile the library, and the Python extension beside it. The library takes nvcc alone; where
+    the extension cannot be compiled (no torch, no Python headers), that is a warning, and the
+    calls that go through it raise."""
+    build_library(force, verbose)
+    try:
+        build_binding(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        if not isinstance(e, ImportError) and os.path.exists(BINDING):
+            os.remove(BINDING)                         # an older one, which may not fit the library
+        warnings.warn(f"no Python extension for the rotary and 4-bit cache calls: {e}")
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile every CUDA source into one shared library (objects built in parallel)."""
     if not force and not _stale():
         return LIB
     objdir = os.path.join(ROOT, "_build")

@@ -369,3 +369,22 @@ def test_a_binding_for_another_torch_is_built_again_and_not_used(lib, monkeypatc
     monkeypatch.setattr(sage, "_calls", None)
     with pytest.raises(RuntimeError, match="is built for"):
         sage.rope(torch.zeros((1, 1, 64), dtype=torch.float16), None, torch.zeros(32, dtype=torch.float64))
+
+
+def test_the_library_is_built_without_the_binding(lib, monkeypatch, tmp_path):
+    from quantized_attention_03_b200 import build
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    real = build.subprocess.run
+
+    def no_headers(cmd, **kw):
+        if cmd[0] == "g++":
+            cmd = ["false"]
+        return real(cmd, **kw)
+
+    monkeypatch.setattr(build.subprocess, "run", no_headers)
+    with pytest.warns(UserWarning, match="no Python extension"):
+        assert build.build() == build.LIB
+    assert not (tmp_path / "_binding.so").exists()
+    monkeypatch.setitem(sys.modules, "torch", None)     # nor is torch needed for it
+    with pytest.warns(UserWarning, match="no Python extension"):
+        assert build.build() == build.LIB
