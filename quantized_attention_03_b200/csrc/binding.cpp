@@ -10,9 +10,11 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <exception>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -494,9 +496,9 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n)
         return F(Args{args});
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const std::exception &e) {
+    } catch (...) {                                    // torch's own errors as Python knows them
         if (!PyErr_Occurred())
-            PyErr_SetString(PyExc_RuntimeError, e.what());
+            torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -633,6 +633,14 @@ def test_what_a_call_allocates_belongs_to_its_stream():
     ok()
 
 
+def test_memory_that_is_not_there_is_torchs_error():
+    # 140 TB of outputs: refused by the allocator before anything runs
+    w = World([4], [4], 2, 64, 16)
+    with pytest.raises(torch.OutOfMemoryError):
+        sage.kv4_gather(w.cache.cuda(), *w.where(), 2 ** 31 - 1, 64, rep=256)
+    ok()
+
+
 def test_a_serving_loop_in_a_graph():
     """Prompt by append, gather and the package's own prefill attention; then decode steps,
     each an append and an attention captured once and replayed with new lengths."""
