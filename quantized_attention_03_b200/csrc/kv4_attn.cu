@@ -25,7 +25,7 @@
 //     step so far, whose product with p = 1 then is 8 or more: two terms are good to 2^-21 of the
 //     product or to 2^-25, which is 2^-28 of the largest step, whichever is more. (One scale for both groups of d = 128
 //     took a group whose values were 10^6 times smaller to 7 bits; two cost the longest cache
-//     2.4 us of 245 and saved the ragged sequences below 0.7 of 81.4.)
+//     1.2 us of 245.0 and saved the ragged sequences below 0.8 of 81.4.)
 // Queries are the 8-wide side of mma.m16n8k16 and keys (or channels) the 16-wide one, so a
 // group of up to 8 query rows that share a key head costs one pass; the 64-row or 128-row
 // tiles of tcgen05 would be almost empty here and could take the codes only from shared
@@ -579,15 +579,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
             }
         }
         const float2 low_sel = t4 < 2 ? make_float2(0.0f, 0.0f) : make_float2(-1.0f, -1.0f);
-        // exponents the value products are scaled for, one for each group of channels, so that a
-        // group of small values keeps its bits beside one of large ones; steps from vlimit on (as
-        // fp16 bits) are too large for it
-        int vexp[kG];
+        // what the value products are scaled by, for each group of channels, so that a group of small
+        // values keeps its bits beside one of large ones, and the steps (as fp16 bits) from which on
+        // they are too large for it: 4 exponents above the one it is made for; 0: for none yet
         uint32_t vlimit[kG];
         float vscale[kG];
 #pragma unroll
         for (int gr = 0; gr < kG; gr++) {
-            vexp[gr] = -64;
             vlimit[gr] = 0;
             vscale[gr] = 1.0f;
         }
@@ -697,9 +695,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
                     for (int gr = 0; gr < kG; gr++) {
                         const int texp = (int)(__reduce_max_sync(0xffffffffu, vtop[gr]) >> 10);
                         shift[gr] = 1.0f;
-                        if (texp > vexp[gr] + 3) {
-                            shift[gr] = vexp[gr] < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp[gr] - texp) << 23);
-                            vexp[gr] = texp;
+                        const int vexp = (int)(vlimit[gr] >> 10) - 4;
+                        if (texp > vexp + 3) {
+                            shift[gr] = vexp < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + vexp - texp) << 23);
                             vlimit[gr] = (uint32_t)(texp + 4) << 10;
                             vscale[gr] = __uint_as_float((uint32_t)(127 + 18 - texp) << 23);
                         }
@@ -866,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT, FOLD>::kCtasPerSM)) kv4_
         float unscale[kG];
 #pragma unroll
         for (int gr = 0; gr < kG; gr++)
-            unscale[gr] = vexp[gr] < 0 ? 0.0f : __uint_as_float((uint32_t)(127 + 6 + vexp[gr]) << 23);
+            unscale[gr] = vlimit[gr] == 0 ? 0.0f : __uint_as_float((127u + 2 + (vlimit[gr] >> 10)) << 23);
         float *const part = p.part + (int64_t)(team * 2 + (seg.t0 == 0)) * (C::kRows * C::kPitch);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
