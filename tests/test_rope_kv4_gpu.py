@@ -633,6 +633,49 @@ def test_what_a_call_allocates_belongs_to_its_stream():
     ok()
 
 
+def test_the_c_calls_by_address():
+    # the entry points of sage.h as they are, which the tensor calls make for their tensors
+    d, Hq, Hkv, page, dt = 64, 4, 2, 16, sage.SAGE_BF16
+    w = World([70, 5, 33], [2, 1, 2], Hkv, d, page, seed=18)
+    w.fill()
+    fused = torch.randn((w.total, Hq + 2 * Hkv, d), generator=w.g).to(BF16).cuda()
+    q, k, v = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    freqs, m = sage.rope_freqs(d, scaling="linear", factor=2.0)
+    table, kv_lens, cu = w.where()
+    seqs = (len(w.lens), w.total)
+    sizes = (page, w.pages, table.shape[1])
+    row = fused.shape[1] * d
+    pos = w.positions().to(torch.int32).cuda()
+
+    rq, rk = torch.empty_like(q), torch.empty_like(k)
+    one = [0, d, row]
+    sage.sage_rope(q, rq, k, rk, pos, freqs, dt, 1, w.total, Hq, Hkv, d, d, 0,
+                   one + [0, d, Hq * d] + one + [0, d, Hkv * d], m, 0)
+    want = sage.rope(q, k, freqs, pos, m)
+    assert torch.equal(rq, want[0]) and torch.equal(rk, want[1])
+
+    a, b = w.cache.cuda(), w.cache.cuda()
+    qo = torch.empty_like(q)
+    sage.sage_kv4_append(a, table, kv_lens, cu, k, v, q, qo, freqs, None, dt, *seqs, Hq, Hkv, d, *sizes, d,
+                         [row, d] * 3 + [Hq * d, d], m, 0)
+    assert torch.equal(qo, sage.kv4_append(b, table, kv_lens, cu, k, v, q, freqs, m)) and torch.equal(a, b)
+    assert torch.equal(qo, rq)
+
+    ko, vo = (torch.empty((w.total, Hkv * 2, d), dtype=BF16, device="cuda") for _ in range(2))
+    sage.sage_kv4_gather(a, table, kv_lens, cu, ko, vo, dt, *seqs, Hkv, 2, d, *sizes)
+    want = sage.kv4_gather(a, table, kv_lens, cu, w.total, d, BF16, 2)
+    assert torch.equal(ko, want[0]) and torch.equal(vo, want[1])
+
+    out, lse = torch.empty_like(qo), torch.empty((w.total, Hq), device="cuda")
+    ws = torch.empty(sage.sage_attn_kv4_workspace_size(Hq, Hkv, 2, d), dtype=torch.uint8, device="cuda")
+    sage.sage_attn_kv4(qo, a, table, kv_lens, cu, out, lse, dt, *seqs, 2, Hq, Hkv, d, *sizes, True, 0.0, None, ws,
+                       ws.numel())
+    ok()
+    w.cache = a.cpu()
+    check_attn(w, qo.cpu(), out, lse)
+    assert torch.equal(out, sage.attn_kv4(qo, a, table, kv_lens, cu, 2))
+
+
 def test_memory_that_is_not_there_is_torchs_error():
     # 140 TB of outputs: refused by the allocator before anything runs
     w = World([4], [4], 2, 64, 16)
