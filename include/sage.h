@@ -385,8 +385,9 @@ SAGE_API sage_status_t sage_rope(const void *q, void *q_out, const void *k, void
  * The 4-bit cache. Each token of a key or value head is cut into groups of 64 channels. With
  * lo and hi a group's least and greatest value: step = fp16((hi - lo) / 15), low = fp16(lo),
  * code = round-half-even((x - low) / step) clamped to 0..15 (0 where step is 0), in fp32 (the
- * division by 15 as a product with its fp32 reciprocal); the group stands for low + code * step. A group that holds a NaN, an infinity or a value past
- * fp16's range stands for non-finite values, and so does an output that sees it.
+ * division by 15 as a product with its fp32 reciprocal); the group stands for low + code * step.
+ * A group that holds a NaN, an infinity or a value past fp16's range stands for non-finite values,
+ * and so does an output that sees it.
  *
  * cache [num_pages, Hkv, sage_kv4_page_bytes(page_size, d)] bytes, 16-byte aligned. A page of
  * a head holds page_size tokens (a power of two, 16 to 256): key codes [page_size][d/2]
@@ -409,8 +410,8 @@ SAGE_API size_t sage_kv4_page_bytes(int page_size, int d);
 /*
  * Append: rows of k and v [total,Hkv,d] become the last tokens of their sequences, k rotated
  * by the tokens' positions (rot_dim = 0: not at all) and, with k_mean (fp32 [Hkv,d], e.g. the
- * channel means of calibration prompts), lessened by it after the rotation: attention does
- * not change when every key of a head is moved by the same vector, and a key's 4-bit range is
+ * channel means of calibration prompts), lessened by it after the rotation: attention's output
+ * does not change (its lse does) when every key of a head is moved by the same vector, and a key's 4-bit range is
  * not spent on a channel offset (the smoothing of step 1 for a cache that grows). q
  * [total,Hq,d] is rotated to q_out alike, or NULL. strides: {token, head} of k, v, q, q_out
  * (8 values), or NULL for contiguous tensors. q_out may be q with the same strides (as
@@ -442,11 +443,19 @@ SAGE_API sage_status_t sage_kv4_gather(const void *cache, const int32_t *block_t
  * cache: query head h reads key head h / (Hq/Hkv). A sequence has at most max_q <=
  * SAGE_DECODE_MAX_Q queries; its query i of n sees keys j <= kv_len - n + i (causal) or all
  * of them. out [total,Hq,d] may be q where that is contiguous, and overlaps nothing else; lse
- * (fp32 [total,Hq], natural log of the sum of exp, or NULL). A query that sees no key gets zeros and -inf. sm_scale <= 0 selects 1/sqrt(d). Scores and
- * softmax are fp32; probabilities enter the value product as two fp16 terms (21 bits).
- * Results do not depend on timing. workspace: device memory of
- * sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) bytes (at most 21 MB), 16-byte aligned, whose contents
- * need not be kept between calls; calls that can overlap need one each.
+ * (fp32 [total,Hq], or NULL) takes the natural log of the sum of exp. A query that sees no key
+ * gets zeros and -inf. Keys that append lessened by k_mean leave out unchanged and make lse
+ * smaller by sm_scale q.k_mean: log-sums of parts go together only where their keys were lessened
+ * alike. sm_scale <= 0 selects 1/sqrt(d).
+ * Precision: sums are fp32. A score is good to 2^-18 of sm_scale sum |q| (|low| + 15 step), the
+ * exponential is the hardware's (2^-22). Weights times value steps enter the value product as two
+ * fp16 terms, good to 2^-21 of each product or to 2^-28 of the largest step of the group (64
+ * channels) that the sequence's queries have seen, whichever is more. Results do not depend on
+ * timing.
+ * workspace: device memory of sage_attn_kv4_workspace_size(Hq, Hkv, max_q, d) bytes (at most
+ * 21 MB), 16-byte aligned, whose contents need not be kept between calls; calls that can overlap
+ * need one each. max_q decides how many rows of a key head a pass takes, so the least that holds
+ * is the fastest: one query a sequence takes 1.7 to 1.8 times as long with 16.
  */
 SAGE_API size_t sage_attn_kv4_workspace_size(int Hq, int Hkv, int max_q, int d);
 SAGE_API sage_status_t sage_attn_kv4(const void *q, const void *cache, const int32_t *block_table,

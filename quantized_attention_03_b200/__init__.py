@@ -749,7 +749,8 @@ def kv4_append(cache, block_table, kv_lens, cu_seqlens, k, v, q=None, freqs=None
     """Writes new tokens' k and v [T, Hkv, d] (any token and head strides) into the paged 4-bit
     cache as the last tokens of their sequences, k rotated by their positions (freqs, mscale:
     rope_freqs; None: not rotated) and lessened by k_mean [Hkv, d]; returns q [T, Hq, d] rotated
-    alike, or None. kv_lens int32 [nseq] counts the new tokens, cu_seqlens int32 [nseq+1] says
+    alike, or None; k_mean leaves attn_kv4's output as it is and its lse smaller. No gradient
+    passes. kv_lens int32 [nseq] counts the new tokens, cu_seqlens int32 [nseq+1] says
     which rows are whose (None: T / nseq each), block_table int32 [nseq, max_pages] where the
     pages are."""
     return _done("sage_kv4_append", (_calls or _bound()).kv4_append(
@@ -775,10 +776,12 @@ def attn_kv4(q, cache, block_table, kv_lens, cu_seqlens=None, max_q: Optional[in
              causal: bool = True, sm_scale: float = 0.0, out=None, lse=None, workspace=None,
              stream=None):
     """Attention of q [T, Hq, d] (any token and head strides) over the paged 4-bit cache; query
-    head h reads key head h // (Hq / Hkv). A sequence has at most max_q queries (by default T /
-    nseq without cu_seqlens, else DECODE_MAX_Q), which are its last tokens. lse: float32 [T, Hq]
-    that takes the log of the softmax sums. The workspace is allocated here unless given; what is
-    allocated belongs to the stream that the call runs on."""
+    head h reads key head h // (Hq / Hkv). A sequence has at most max_q queries, which are its
+    last tokens (by default T / nseq without cu_seqlens, else DECODE_MAX_Q: give the least that
+    holds, since one query a sequence takes 1.7 to 1.8 times as long with 16). lse: float32
+    [T, Hq] that takes the log of the softmax sums, over keys as the cache holds them (lessened by
+    k_mean). The workspace is allocated here unless given; what is allocated belongs to the stream
+    that the call runs on. No gradient passes, as none does in the package's attention."""
     return _done("sage_attn_kv4", (_calls or _bound()).attn_kv4(
         q, cache, block_table, kv_lens, cu_seqlens, max_q, causal, sm_scale, out, lse, workspace,
         None if stream is None else _stream(stream)))

@@ -10,10 +10,13 @@
 // What bounds it: the cache is read once from HBM, 0.5625 bytes per element (B8 H32 over 32768
 // keys of d 128: 1.21 GB, 185 us at the copy bandwidth, which the copies alone reach), and each
 // element has to be turned from 4 bits into a 16-bit operand: the instructions are the bound,
-// 231 us for that cache without its copies, 245 us in all (4.9 TB/s).
+// 231 us for that cache without its copies, 246 us in all (4.9 TB/s; 272 us in a loop of calls that
+// lasts, at the lower clock of that).
 //   - A code masked in place is an fp16 subnormal, n 2^-24 or 16 n 2^-24, which the tensor core
 //     takes as it is; one AND makes two operands. The queries of the second kind of channel are
-//     divided by 16 beforehand, the outputs at the end. Sums of such products are good to 2^-18.
+//     divided by 16 beforehand, the outputs at the end. Sums of such products are good to 2^-18 of
+//     their terms' absolute sum; fp16 outputs over random keys are 2.1e-4 from 64-bit results, as
+//     those rounded to fp16 are.
 //   - Values are centred (n - 8), because the sum of p n' stays near the size of its result;
 //     uncentred it would be the difference of two sums 100 times larger over a long cache, in
 //     which the accumulator's own rounding shows. One product with constant codes -8 gives what
@@ -23,13 +26,14 @@
 //     product: one term alone would round every p to 11 bits, as much error again as the
 //     rounding of the 16-bit output. They are scaled by a power of two of their group's largest
 //     step so far, whose product with p = 1 then is 8 or more: two terms are good to 2^-21 of the
-//     product or to 2^-25, which is 2^-28 of the largest step, whichever is more. (One scale for both groups of d = 128
-//     took a group whose values were 10^6 times smaller to 7 bits; two cost the longest cache
-//     1.2 us of 245.0 and saved the ragged sequences below 0.8 of 81.4.)
+//     product or to 2^-25, which is 2^-28 of the largest step, whichever is more. (One scale for
+//     both groups of d = 128 left a group whose values were 10^6 times smaller 7 bits; two cost the
+//     longest cache 1.2 us of 245.0 and saved the ragged sequences below 0.8 of 81.4.)
 // Queries are the 8-wide side of mma.m16n8k16 and keys (or channels) the 16-wide one, so a
-// group of up to 8 query rows that share a key head costs one pass; the 64-row or 128-row
-// tiles of tcgen05 would be almost empty here and could take the codes only from shared
-// memory, expanded to bytes.
+// group of up to 8 query rows that share a key head costs one pass, and a masked word of codes is
+// an operand where it was loaded. tcgen05 was not tried: with keys on its 128-row side and 8 to 32
+// rows of queries as N its tiles would be full, but its operands lie in shared or tensor memory, so
+// the codes would first be expanded and written there.
 //
 // Work split: all (sequence, key head, row block, tile) of the call form one list, cut into
 // equal shares whatever the sequences' lengths (which only the device knows), one per team: a
@@ -76,8 +80,8 @@ struct Cfg {
     static constexpr int kTile = 4096 / D;             // keys per warp tile
     static constexpr int kGroups = D / kKv4Group;
     static constexpr int kStages = 2;                  // of 32 or 64 keys: 55 KB an SM in flight
-    // 12 warps of 168 registers or 8 of 255; 16 of 128 registers spill: 98 against 86 us over the
-    // ragged sequences below
+    // 12 warps of 168 registers or 8 of 255 (50 to 80 bytes of spills a thread at d = 128); 16 of
+    // 128 registers (200 to 220 bytes): 98 against 86 us over the ragged sequences below
     static constexpr int kCtasPerSM = NT == 1 ? 3 : 2;
     static constexpr int kRows = FOLD ? 4 : 8 * NT;
     static constexpr int kParBytes = kTile * kGroups * 4;          // params of a tile's keys
