@@ -194,6 +194,13 @@ void want_places(const Tensor &out, const char *what)
     want(out.numel() == 0 || dims_of(out, out, d) >= 0, out, what);
 }
 
+// Autograd learns that a tensor it may have saved is written over.
+void written(const Tensor &x)
+{
+    if (!x.is_inference())
+        x.unsafeGetTensorImpl()->bump_version();
+}
+
 // The device of the call's tensors and the stream given (a pointer) made current, so that what
 // the call allocates belongs to the stream that uses it: a workspace is free again when the call
 // returns, and only that stream's order keeps the kernel's use before the next one's.
@@ -317,6 +324,10 @@ PyObject *rope(const Args &a)
         s, a.real(4), (a.truth(5) ? SAGE_ROPE_INTERLEAVED : 0) | (a.truth(6) ? SAGE_ROPE_INVERSE : 0), w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
+    if (!a.none(7))
+        written(q_out);
+    if (has_k && !a.none(8))
+        written(k_out);
     PyObject *qo = THPVariable_Wrap(std::move(q_out));
     PyObject *ko = has_k ? THPVariable_Wrap(std::move(k_out)) : Py_NewRef(Py_None);
     return Py_BuildValue("(NN)", qo, ko);
@@ -408,6 +419,8 @@ PyObject *append(const Args &a)
         a.truth(9) ? SAGE_ROPE_INTERLEAVED : 0, w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
+    if (q && !a.none(11))
+        written(q_out);
     return q ? THPVariable_Wrap(std::move(q_out)) : Py_NewRef(Py_None);
 }
 
@@ -440,6 +453,9 @@ PyObject *gather(const Args &a)
                                       s.Hkv, rep, d, s.page_size, s.num_pages, s.max_pages, w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
+    for (int i : {8, 9})
+        if (!a.none(i))
+            written(i == 8 ? k : v);
     PyObject *ko = THPVariable_Wrap(std::move(k)), *vo = THPVariable_Wrap(std::move(v));
     return Py_BuildValue("(NN)", ko, vo);
 }
@@ -483,6 +499,10 @@ PyObject *attn(const Args &a)
                (float)a.real(7), st, ws.mutable_data_ptr(), ws.nbytes(), w.stream());
     if (rc != SAGE_OK)
         return PyLong_FromLong(rc);
+    if (!a.none(8))
+        written(out);
+    if (lse)
+        written(a.tensor(9, "lse"));
     return THPVariable_Wrap(std::move(out));
 }
 

@@ -213,6 +213,34 @@ def test_rope_gradient_twice_on_a_stream_and_after_its_inputs_changed():
     ok()
 
 
+def test_autograd_sees_that_outputs_are_written_over():
+    # each output once where a product has saved it: its gradient cannot be had any more
+    w = World([9, 30], [1, 1], 2, 64, 16, seed=19)
+    w.fill()
+    cache, where = w.cache.cuda(), w.where()
+    freqs, _ = sage.rope_freqs(64)
+    q, k = (torch.randn((2, h, 64), generator=w.g).to(F16).cuda() for h in (4, 2))
+    pos = torch.arange(2, dtype=torch.int32).cuda()
+    lse = torch.zeros((2, 4), device="cuda")
+    for name, out, call in (
+            ("q_out", q, lambda x: sage.rope(x, None, freqs, pos, q_out=x)),
+            ("k_out", k, lambda x: sage.rope(q, x, freqs, pos, k_out=x)),
+            ("append", q, lambda x: sage.kv4_append(cache, *where, k, k, x, freqs, q_out=x)),
+            ("gather k", k, lambda x: sage.kv4_gather(cache, *where, 2, 64, k_out=x)),
+            ("gather v", k, lambda x: sage.kv4_gather(cache, *where, 2, 64, v_out=x)),
+            ("attention", q, lambda x: sage.attn_kv4(q, cache, *where, 1, out=x)),
+            ("lse", lse, lambda x: sage.attn_kv4(q, cache, *where, 1, lse=x))):
+        saved = out.clone()
+        leaf = torch.ones_like(saved, requires_grad=True)
+        product = leaf * saved
+        call(saved)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            product.sum().backward()
+        with torch.inference_mode():                    # tensors without versions
+            call(out.clone())
+    ok()
+
+
 def test_rope_gradient_in_a_captured_graph():
     g = torch.Generator().manual_seed(7)
     x, y = (torch.randn((33, 4, 128), generator=g).to(BF16).cuda() for _ in range(2))
