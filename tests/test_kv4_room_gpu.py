@@ -129,3 +129,21 @@ def test_sharp_scores_and_queries_of_very_different_size(d, Hq):
     q = torch.randn((w.total, Hq, d), generator=w.g) * 10.0 ** torch.randint(-3, 2, (w.total, Hq, 1), generator=w.g)
     q = q.to(F16)
     check(w, q, *attend(w, q, 2, sm_scale=0.5), sm_scale=0.5)
+
+
+@pytest.mark.parametrize("nseq,Hq,new", [(3, 4, 1), (3, 32, 5), (90, 4, 1), (90, 16, 3), (90, 32, 5)])
+def test_the_output_over_the_queries(nseq, Hq, new):
+    # a row is read by the one segment that writes it, in CTAs and in warps that work alone
+    g = torch.Generator().manual_seed(nseq + Hq)
+    lens = torch.randint(new, 300, (nseq,), generator=g).tolist()
+    lens[0] = 3000
+    w = World(lens, [new] * nseq, 2, 128, 16, seed=39)
+    w.fill()
+    q = torch.randn((w.total, Hq, 128), generator=w.g).to(F16).cuda()
+    cache, where = w.cache.cuda(), w.where()
+    want = sage.attn_kv4(q, cache, *where, new)
+    for _ in range(5):
+        x = q.clone()
+        assert sage.attn_kv4(x, cache, *where, new, out=x) is x
+        assert torch.equal(x, want)
+    ok()
