@@ -406,23 +406,26 @@ def _smooth_flags(smooth_k: bool, smooth_v: bool, fine: bool = False,
             | (SAGE_QK_FINE if fine else 0) | (SAGE_SMOOTH_Q if smooth_q else 0))
 
 
-def _want_fp16(q, k=None, v=None, out=None):
-    """What goes to the attention and quantization kernels by address alone is contiguous
-    float16, and k and v have q's heads and channels (and a dense q's batch), and one length."""
+def _want_fp16(*tensors):
+    """What goes to the attention and quantization kernels by address alone is contiguous float16."""
     import torch
-    for x in (q, k, v, out):
+    for x in tensors:
         if x is not None and (x.dtype is not torch.float16 or not x.is_contiguous()):
             raise ValueError(f"contiguous float16 tensors are wanted, got {x.dtype} {tuple(x.shape)} with "
                              f"strides {x.stride()}")
 
-    def heads(x):
-        return x.shape[1:] if x.dim() == 3 else x.shape[:2] + x.shape[3:]
 
-    if k is not None and (k.dim() != q.dim() or heads(k) != heads(q)):
-        raise ValueError(f"k has q's heads and channels, got {tuple(k.shape)} and {tuple(q.shape)}")
-    if v is not None and k is not None and v.shape != k.shape:
-        raise ValueError(f"v has k's shape, got {tuple(v.shape)} and {tuple(k.shape)}")
-    if out is not None and out.shape != q.shape:
+def _want_size(name: str, x, n: int, like=None):
+    """x holds the n elements that a kernel takes from its address on; more only as further rows
+    of packed tensors like `like`."""
+    if x.numel() != n and not (like is not None and x.numel() > n and x.shape[1:] == like.shape[1:]):
+        raise ValueError(f"{name} of {n} elements is wanted (k and v with q's heads and channels), got "
+                         f"{tuple(x.shape)}")
+
+
+def _want_out(out, q):
+    _want_fp16(out)
+    if out.numel() < q.numel():
         raise ValueError(f"out has q's shape, got {tuple(out.shape)} and {tuple(q.shape)}")
 
 
@@ -434,9 +437,13 @@ def sageattn(q, k, v, causal: bool = False, smooth_k: bool = True, pv_mode: int 
     import torch
     B, H, Nq, d = q.shape
     Nk = k.shape[2]
-    _want_fp16(q, k, v, out)
+    _want_fp16(q, k, v)
+    _want_size("k", k, B * H * Nk * d)
+    _want_size("v", v, B * H * Nk * d)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _want_out(out, q)
     flags = _smooth_flags(smooth_k, smooth_v, fine, smooth_q)
     if Nq == Nk:
         sage_attn_fwd(q, k, v, out, B, H, Nq, d, causal, flags, pv_mode, sm_scale, stream)
@@ -457,9 +464,13 @@ def sageattn_varlen_kv(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, m
     import torch
     Tq, H, d = q.shape
     Tk = k.shape[0]
-    _want_fp16(q, k, v, out)
+    _want_fp16(q, k, v)
+    _want_size("k", k, Tk * H * d)
+    _want_size("v", v, Tk * H * d, k)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _want_out(out, q)
     sage_attn_varlen_fwd_kv(q, k, v, out, cu_seqlens_q, cu_seqlens_k, cu_seqlens_q.numel() - 1,
                             Tq, Tk, max_seqlen_q, max_seqlen_k, H, d, causal,
                             _smooth_flags(smooth_k, smooth_v, fine, smooth_q), pv_mode, sm_scale,
@@ -475,11 +486,13 @@ def sageattn_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False,
     The options are sageattn's."""
     import torch
     T, H, d = q.shape
-    _want_fp16(q, k, v, out)
-    if k.shape != q.shape:
-        raise ValueError(f"k has q's shape, got {tuple(k.shape)} and {tuple(q.shape)}")
+    _want_fp16(q, k, v)
+    _want_size("k", k, T * H * d, q)
+    _want_size("v", v, T * H * d, q)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _want_out(out, q)
     sage_attn_varlen_fwd(q, k, v, out, cu_seqlens, cu_seqlens.numel() - 1, T, max_seqlen, H, d,
                          causal, _smooth_flags(smooth_k, smooth_v, fine, smooth_q), pv_mode,
                          sm_scale, None, 0, stream)
@@ -495,6 +508,7 @@ def quant_qk(q, k, smooth_k: bool = True, stream=None, fine: bool = False,
     B, H, N, d = q.shape
     Nk = k.shape[2]
     _want_fp16(q, k)
+    _want_size("k", k, B * H * Nk * d)
     dev = q.device
     qg, kg = (1, 32) if fine else (Q_BLOCK, K_BLOCK)
     z = dict(q_i8=torch.empty(q.shape, dtype=torch.int8, device=dev),
@@ -523,6 +537,7 @@ def quant_qk_varlen(q, k, cu_seqlens, max_seqlen: int, smooth_k: bool = True, st
     T, H, d = q.shape
     nseq = cu_seqlens.numel() - 1
     _want_fp16(q, k)
+    _want_size("k", k, T * H * d, q)
     dev = q.device
     qg, kg = (1, 32) if fine else (Q_BLOCK, K_BLOCK)
     z = dict(q_i8=torch.empty(q.shape, dtype=torch.int8, device=dev),

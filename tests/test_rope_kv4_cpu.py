@@ -388,3 +388,20 @@ def test_the_library_is_built_without_the_binding(lib, monkeypatch, tmp_path):
     monkeypatch.setitem(sys.modules, "torch", None)     # nor is torch needed for it
     with pytest.warns(UserWarning, match="no Python extension"):
         assert build.build() == build.LIB
+
+
+def test_fp16_calls_take_the_same_memory_in_another_shape(lib, monkeypatch):
+    # what the kernels read and write is there, whatever the tensors' shapes say beyond it
+    half = lambda *shape: torch.zeros(shape, dtype=torch.float16)  # noqa: E731
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    made = []
+    monkeypatch.setattr(sage, "_call", lambda name, *args: made.append(name))
+    monkeypatch.setattr(sage, "_stream", lambda s: 0)
+    q, dq, dk = half(4, 4, 64), half(2, 4, 4, 64), half(2, 4, 8, 64)
+    sage.sageattn(dq, dk, dk.view(8, 8, 64), out=half(8, 4, 64))
+    sage.sageattn(dq, half(1, 8, 8, 64), dk)
+    sage.sageattn_varlen(q, half(9, 4, 64), half(9, 4, 64), cu, 4, out=half(6, 4, 64))
+    sage.sageattn_varlen_kv(q, half(9, 4, 64), half(12, 4, 64), cu, cu, 4, 4, out=half(4, 256))
+    sage.quant_qk(dq, half(1, 8, 8, 64))
+    sage.quant_qk_varlen(q, half(9, 4, 64), cu, 4)
+    assert len(made) == 6
